@@ -372,6 +372,129 @@ ZT_API int zt_q4_gemm_f16w_gate_up_silu(const uint16_t *w16, const uint16_t *x, 
                                         void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * PAGED 4-BIT KV CACHE
+ *
+ * Zero-TVM write-up, "完整的推理流水线": a paged KV cache that the fused QKV kernel
+ * appends to and attention reads through a page table (and, as an option, a
+ * narrower cache).  The pages give no format for a narrow cache; this library
+ * keeps K and V in its own q4f16 reading: 4-bit codes, value = (code - 7) * scale,
+ * one fp16 scale per 32 values of a token's head.
+ *
+ * A pool holds n_pages pages of page_size tokens.  A page holds, for each kv
+ * head, page_size / 16 tiles of 16 tokens; a tile of head_dim D is 18 D bytes:
+ * K codes (8 D bytes), V codes (8 D), K scales (D), V scales (D).  With G = D/32:
+ *   K code of token t, d = 32 g + 8 j + n:               nibble n of word t*D/8 + j*G + g
+ *   V code of token t = 8 h + 2 j + e, d = 16 m + 8 i + r: nibble i of byte 2 e + h
+ *                                                        of word (m/2)*64 + (4 r + j)*2 + m%2
+ *   K scale of token t = 8 h + r, group g:               half (r*G + g)*2 + h
+ *   V scale of token t = 8 h + 2 j + e, group g:         half ((j*G + g)*2 + h)*2 + e
+ * (the order in which the attention kernel's matrix instructions take them).
+ * A row is quantized per group of 32 values x:
+ *   s = fp16(max(max x / 8, -min x / 7)),  code = clamp(round(x / s) + 7, 0, 15)
+ * (round to nearest even; s = 0: code 7; a group with an infinity or a NaN gets
+ * s = NaN and reads back as NaN).
+ *
+ * Sequences are rows of a page table, int32 [n_seqs][max_pages] (DEVICE): the
+ * token at position p of sequence b is in page table[b][p / page_size].  Entries
+ * that no valid position reaches are never read.  Pages may appear in several
+ * rows (shared prefixes); a page that is being appended to must not.
+ *
+ * Indices live on the device, so they are checked there: a page index, position
+ * or sequence out of range sets bit 0 (ZT_Q4_KV_ERR_PLACE) of *err and that row
+ * or tile is left out; bit 1 (ZT_Q4_KV_ERR_WAIT) reports a bounded wait (2 s)
+ * that ran out.  err (DEVICE, 4-byte aligned, may be NULL) is only ever OR-ed
+ * into: the caller clears it, once, and reads it when it likes
+ * (zt_q4_kv_errors, synchronous).
+ *
+ * The kernels of this section read nothing before the kernel ahead of them on
+ * the stream has completed.
+ */
+#define ZT_Q4_KV_ERR_PLACE 1u
+#define ZT_Q4_KV_ERR_WAIT 2u
+#define ZT_Q4_KV_MAX_SEQS 4096
+
+typedef struct zt_q4_kv {
+    void *pages;              /* DEVICE, 16-byte aligned: n_pages pages of zt_q4_kv_page_bytes() bytes */
+    int n_pages;
+    int page_size;            /* tokens: a multiple of 16, 16..1024 */
+    int kv_heads;             /* 1..1024 */
+    int head_dim;             /* 64, 96 or 128 */
+    uint32_t *err;            /* DEVICE error word, or NULL */
+} zt_q4_kv;
+
+/* Rows of an append or a gather: row i belongs at position pos[i] of sequence seq[i] (DEVICE, int32 [n]).
+ * pos[i] < 0 marks padding: the row is skipped, what it would write is left as it was. */
+typedef struct zt_q4_kv_rows {
+    const int32_t *seq, *pos;
+    int n;                    /* 0..2^24 */
+    const int32_t *page_table;
+    int n_seqs, max_pages;
+} zt_q4_kv_rows;
+
+/* Optional rotary embedding of an append, the rotation of zt_q4_rope on halves i and i + head_dim/2 (angle,
+ * sin and cos in double, then rounded to fp32; each product and sum of the rotation rounded in fp32; fp16 at
+ * the end): k is rotated before it is quantized, from its fp16 value, and q [n][ld_q], if given, is rotated too. */
+typedef struct zt_q4_kv_rope {
+    float theta;              /* > 0 */
+    const uint16_t *q;        /* fp16 [n][ld_q], q_heads * head_dim values per row, or NULL */
+    int ld_q, q_heads;
+    uint16_t *q_out;          /* fp16 [n][ld_q_out], with q; q itself is not allowed */
+    int ld_q_out;
+    uint16_t *k_out;          /* fp16 [n][ld_k_out] receives the rotated k, or NULL */
+    int ld_k_out;
+} zt_q4_kv_rope;
+
+/* Bytes of one page; 0 for sizes out of range. */
+ZT_API size_t zt_q4_kv_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/*
+ * Appends rows to the cache: k and v fp16 [n][ld] (kv_heads * head_dim values per
+ * row; strides in elements, multiples of 8; 16-byte aligned) are quantized into
+ * their places, rotated first if rope is given.  Places must be distinct.
+ * Rows already in a tile stay as they are.  One launch.
+ */
+ZT_API int zt_q4_kv_append(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, const uint16_t *k, int ld_k,
+                           const uint16_t *v, int ld_v, const zt_q4_kv_rope *rope, void *stream);
+
+/* Reads rows back: k and v fp16 [n][ld] receive fp16((code - 7) * scale).  Strides and alignment as above. */
+ZT_API int zt_q4_kv_gather(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, uint16_t *k, int ld_k, uint16_t *v,
+                           int ld_v, void *stream);
+
+/*
+ * Copies page src[i] onto page dst[i] (DEVICE, int32 [n], 0 <= n <= 2^24) in each of
+ * `layers` pools that lie layer_bytes apart from kv->pages on (a multiple of 16; any
+ * value when layers is 1).  No page may be both a destination and another entry's
+ * source or destination (which content arrives would depend on timing).
+ */
+ZT_API int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int32_t *dst, int n, int layers,
+                               size_t layer_bytes, void *stream);
+
+/*
+ * Attention of the last `tokens` (1..16) tokens of each sequence over the cache,
+ * which already holds them (Zero-TVM write-up, "内核融合": attention.wgsl reads the
+ * page table):
+ *   out[b][i][h] = softmax_t(scale * q[b][i][h] . k[t][h / group]) v[t][h / group],
+ *   t < lens[b] - tokens + i + 1,   group = q_heads / kv_heads.
+ * q and out: fp16, row b * tokens + i of ld_q / ld_out elements (multiples of 8;
+ * q 16-byte, out 2-byte aligned), q_heads * head_dim values each.  lens: int32
+ * [n_seqs] (DEVICE): tokens of each sequence in the cache.  A query that sees no
+ * token gives zeros.  n_seqs <= ZT_Q4_KV_MAX_SEQS; q_heads a multiple of kv_heads.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to fp16
+ * before and after they are multiplied by V's scales.
+ * workspace: DEVICE, 16-byte aligned, zt_q4_kv_attention_workspace_bytes() bytes
+ * (a function of these sizes alone); contents on entry do not matter.  Calls that
+ * may overlap need workspaces of their own.  Two launches.
+ */
+ZT_API size_t zt_q4_kv_attention_workspace_bytes(int kv_heads, int q_heads, int head_dim, int tokens);
+ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, int q_heads, int tokens,
+                              const int32_t *lens, const int32_t *page_table, int n_seqs, int max_pages,
+                              float scale, uint16_t *out, int ld_out, void *workspace, size_t ws_bytes,
+                              void *stream);
+
+/* Synchronous read of an error word (kv->err or the err of zt_q4_prompt_attention). */
+ZT_API int zt_q4_kv_errors(const uint32_t *err, unsigned int *out);
+
+/*
  * Host-side layout helpers (HOST pointers, synchronous, no CUDA calls).
  * pack:   q uint8 [N][K] codes 0..15  ->  qw uint32 [N][K/8], low nibble first.
  *         A code above 15 is ZT_ERR_INVALID_ARG (qw is then unspecified).
@@ -392,7 +515,7 @@ ZT_API const char *zt_q4_strerror(int status);
 ZT_API const char *zt_q4_last_cuda_error(void);
 
 /* Library ABI version, (major << 16) | minor.  1.3 added zt_q4_pass_plan; 1.4 its column_blocks; 1.5 its
- * warps_per_cta; 1.6 zt_q4_build_flags and zt_q4_pass_test_cut. */
+ * warps_per_cta; 1.6 zt_q4_build_flags and zt_q4_pass_test_cut; 1.7 the paged 4-bit KV cache (zt_q4_kv_*). */
 ZT_API int zt_q4_version(void);
 
 #ifdef __cplusplus

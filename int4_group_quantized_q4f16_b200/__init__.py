@@ -6,7 +6,8 @@ work on a machine where the library has not been built yet; touching any
 compute name without the library raises ImportError.
 """
 _BINDING = ("gemv", "gate_up_silu", "lmhead_argmax", "lmhead_workspace_bytes",
-            "pack_host", "unpack_host", "strerror", "version", "ZtError")
+            "pack_host", "unpack_host", "strerror", "version", "ZtError",
+            "KvCache", "KvAppend", "KvGather", "KvCopy", "KvAttention", "kv_page_bytes")
 
 
 def __getattr__(name):

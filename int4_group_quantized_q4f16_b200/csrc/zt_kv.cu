@@ -1,0 +1,296 @@
+// zt_kv.cu -- C ABI of the paged 4-bit KV cache and of attention over it (see
+// include/zt_q4.h for the contract of every entry point): argument checks,
+// launch shapes and launches.  Every check runs before the first CUDA call.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "zt_host.h"
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
+#include "zt_q4.h"
+
+namespace {
+
+using namespace zt;
+
+constexpr int kRowsMax = 1 << 24;
+constexpr int kSmsB200 = 148;      // sizes the workspace, so that the query needs no device
+
+int device_error(cudaError_t e, int status)
+{
+    g_last_cuda_error = e;
+    (void)cudaGetLastError();
+    return status;
+}
+
+size_t page_bytes(int page_size, int kv_heads, int head_dim)
+{
+    if (page_size < kKvTile || page_size > 1024 || page_size % kKvTile || kv_heads < 1 || kv_heads > 1024) return 0;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128) return 0;
+    return (size_t)kv_heads * (page_size / kKvTile) * 18 * head_dim;
+}
+
+int check_kv(const zt_q4_kv *kv)
+{
+    if (!kv || !kv->pages || kv->n_pages < 1) return ZT_ERR_INVALID_ARG;
+    if (kv->head_dim != 64 && kv->head_dim != 96 && kv->head_dim != 128) return ZT_ERR_UNSUPPORTED;
+    if (!page_bytes(kv->page_size, kv->kv_heads, kv->head_dim)) return ZT_ERR_INVALID_ARG;
+    if (!aligned(kv->pages, 16) || !aligned(kv->err, 4)) return ZT_ERR_MISALIGNED;
+    return ZT_OK;
+}
+
+// a page table whose positions fit in int
+int check_table(const int32_t *table, int n_seqs, int max_pages, int page_size)
+{
+    if (!table || n_seqs < 1 || max_pages < 1 || (int64_t)max_pages * page_size > INT_MAX) return ZT_ERR_INVALID_ARG;
+    return aligned(table, 4) ? ZT_OK : ZT_ERR_MISALIGNED;
+}
+
+int check_rows(const zt_q4_kv *kv, const zt_q4_kv_rows *rows)
+{
+    if (!rows || rows->n < 0 || rows->n > kRowsMax) return ZT_ERR_INVALID_ARG;
+    if (rows->n && (!rows->seq || !rows->pos)) return ZT_ERR_INVALID_ARG;
+    if (!aligned(rows->seq, 4) || !aligned(rows->pos, 4)) return ZT_ERR_MISALIGNED;
+    return check_table(rows->page_table, rows->n_seqs, rows->max_pages, kv->page_size);
+}
+
+// fp16 rows read and written 16 bytes at a time
+int check_matrix(const void *p, int ld, int64_t width)
+{
+    if (!p || ld < width) return ZT_ERR_INVALID_ARG;
+    return aligned(p, 16) && ld % 8 == 0 ? ZT_OK : ZT_ERR_MISALIGNED;
+}
+
+KvPlaces places(const zt_q4_kv *kv, const int32_t *table, int n_seqs, int max_pages)
+{
+    KvPlaces p;
+    p.pages = static_cast<unsigned char *>(kv->pages);
+    p.page_bytes = (long long)page_bytes(kv->page_size, kv->kv_heads, kv->head_dim);
+    p.n_pages = kv->n_pages;
+    p.page_size = kv->page_size;
+    p.kv_heads = kv->kv_heads;
+    p.table = table;
+    p.n_seqs = n_seqs;
+    p.max_pages = max_pages;
+    p.err = kv->err;
+    return p;
+}
+
+const __half *h(const uint16_t *p) { return reinterpret_cast<const __half *>(p); }
+__half *h(uint16_t *p) { return reinterpret_cast<__half *>(p); }
+
+// Launch with programmatic dependent launch: the kernel may start while the one ahead of it on the
+// stream ends; it waits for it before it reads anything.
+template <typename Args>
+int launch(void (*fn)(Args), dim3 grid, int threads, size_t smem, const Args &args, void *stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    clear_stale_error();
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args);
+    return e == cudaSuccess ? ZT_OK : device_error(e, ZT_ERR_LAUNCH);
+}
+
+// Rows of a few heads leave most SMs idle: a row's values are spread over CTAs until the grid
+// covers the device about twice.
+dim3 row_grid(int rows, int items)
+{
+    const int most = std::max(1, (items + 255) / 256);
+    return dim3((unsigned)rows, (unsigned)std::max(1, std::min(most, 2 * kSmsB200 / std::max(1, rows) + 1)));
+}
+
+size_t part_bytes(int head_dim, int cols8)
+{
+    return (size_t)kSmsB200 * 2 * cols8 * (head_dim + 2) * sizeof(float);
+}
+
+// Columns (query tokens x grouped heads) go through the matrix instruction eight at a time; from nine
+// on, sixteen share one pass over the cache.
+int column_tiles(int cols) { return cols > 8 ? 2 : 1; }
+
+template <int D, int NT>
+int launch_attention(KvAttnArgs &a, void *stream)
+{
+    using C = KvAttnCfg<D, NT>;
+    a.blocks = (a.cols + C::kCols - 1) / C::kCols;
+    const int64_t segments = (int64_t)a.at.n_seqs * a.at.kv_heads * a.blocks;
+    if (segments * a.at.max_pages * (a.at.page_size / kKvTile) > INT_MAX) return ZT_ERR_UNSUPPORTED;
+    const size_t prefix = ((size_t)a.at.n_seqs + 1) * sizeof(int);
+    int sms = 0;
+    if (resident_ctas(reinterpret_cast<const void *>(&kv_attn_kernel<D, NT>), C::kWarps * 32, C::kSmem + prefix, sms) < 1)
+        return ZT_ERR_DEVICE;
+    a.ctas = std::min(sms, kSmsB200);
+    int rc = launch(kv_attn_kernel<D, NT>, dim3((unsigned)a.ctas), C::kWarps * 32, C::kSmem + prefix, a, stream);
+    if (rc) return rc;
+    return launch(kv_attn_join_kernel<D, NT>, dim3((unsigned)segments, (unsigned)std::min(C::kCols, a.cols)), 128, prefix,
+                  a, stream);
+}
+
+template <int D>
+int launch_attention(KvAttnArgs &a, void *stream)
+{
+    return column_tiles(a.cols) == 1 ? launch_attention<D, 1>(a, stream) : launch_attention<D, 2>(a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t zt_q4_kv_page_bytes(int page_size, int kv_heads, int head_dim) { return page_bytes(page_size, kv_heads, head_dim); }
+
+int zt_q4_kv_append(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, const uint16_t *k, int ld_k, const uint16_t *v,
+                    int ld_v, const zt_q4_kv_rope *rope, void *stream)
+{
+    int rc = check_kv(kv);
+    if (!rc) rc = check_rows(kv, rows);
+    if (rc) return rc;
+    const int64_t width = (int64_t)kv->kv_heads * kv->head_dim;
+    if ((rc = check_matrix(k, ld_k, width)) || (rc = check_matrix(v, ld_v, width))) return rc;
+    if (rope) {
+        if (!(rope->theta > 0.f) || rope->theta > 3.0e38f) return ZT_ERR_INVALID_ARG;
+        if (rope->q) {
+            if (rope->q_heads < 1 || rope->q_heads > 16384) return ZT_ERR_INVALID_ARG;
+            const int64_t qw = (int64_t)rope->q_heads * kv->head_dim;
+            if ((rc = check_matrix(rope->q, rope->ld_q, qw)) || (rc = check_matrix(rope->q_out, rope->ld_q_out, qw)))
+                return rc;
+            if (rope->q_out == rope->q) return ZT_ERR_INVALID_ARG;
+        } else if (rope->q_out) {
+            return ZT_ERR_INVALID_ARG;
+        }
+        if (rope->k_out && (rc = check_matrix(rope->k_out, rope->ld_k_out, width))) return rc;
+        if (rope->k_out == k) return ZT_ERR_INVALID_ARG;
+    }
+    if (rows->n == 0) return ZT_OK;
+    KvAppendArgs a = {};
+    a.at = places(kv, rows->page_table, rows->n_seqs, rows->max_pages);
+    a.seq = rows->seq;
+    a.pos = rows->pos;
+    a.k = h(k);
+    a.v = h(v);
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    if (rope) {
+        a.rope = 1;
+        a.q = h(rope->q);
+        a.q_out = h(rope->q_out);
+        a.k_out = h(rope->k_out);
+        a.ld_q = rope->ld_q;
+        a.ld_q_out = rope->ld_q_out;
+        a.ld_k_out = rope->ld_k_out;
+        a.q_heads = rope->q ? rope->q_heads : 0;
+        for (int i = 0; i < kv->head_dim / 2; ++i) a.freq[i] = std::pow((double)rope->theta, -2.0 * i / kv->head_dim);
+    }
+    const dim3 grid = row_grid(rows->n, (2 * kv->kv_heads + a.q_heads) * kv->head_dim / 8);
+    if (kv->head_dim == 64) return launch(kv_append_kernel<64>, grid, 256, 0, a, stream);
+    if (kv->head_dim == 96) return launch(kv_append_kernel<96>, grid, 256, 0, a, stream);
+    return launch(kv_append_kernel<128>, grid, 256, 0, a, stream);
+}
+
+int zt_q4_kv_gather(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, uint16_t *k, int ld_k, uint16_t *v, int ld_v,
+                    void *stream)
+{
+    int rc = check_kv(kv);
+    if (!rc) rc = check_rows(kv, rows);
+    if (rc) return rc;
+    const int64_t width = (int64_t)kv->kv_heads * kv->head_dim;
+    if ((rc = check_matrix(k, ld_k, width)) || (rc = check_matrix(v, ld_v, width))) return rc;
+    if (rows->n == 0) return ZT_OK;
+    KvGatherArgs a = {};
+    a.at = places(kv, rows->page_table, rows->n_seqs, rows->max_pages);
+    a.seq = rows->seq;
+    a.pos = rows->pos;
+    a.k = h(k);
+    a.v = h(v);
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    const dim3 grid = row_grid(rows->n, 2 * kv->kv_heads * kv->head_dim / 8);
+    if (kv->head_dim == 64) return launch(kv_gather_kernel<64>, grid, 256, 0, a, stream);
+    if (kv->head_dim == 96) return launch(kv_gather_kernel<96>, grid, 256, 0, a, stream);
+    return launch(kv_gather_kernel<128>, grid, 256, 0, a, stream);
+}
+
+int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int32_t *dst, int n, int layers,
+                        size_t layer_bytes, void *stream)
+{
+    const int rc = check_kv(kv);
+    if (rc) return rc;
+    if (n < 0 || n > kRowsMax || layers < 1 || layers > 65535) return ZT_ERR_INVALID_ARG;
+    if (n && (!src || !dst)) return ZT_ERR_INVALID_ARG;
+    const size_t bytes = page_bytes(kv->page_size, kv->kv_heads, kv->head_dim);
+    if (layers > 1 && layer_bytes < bytes * (size_t)kv->n_pages) return ZT_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4) || (layers > 1 && layer_bytes % 16)) return ZT_ERR_MISALIGNED;
+    if (n == 0) return ZT_OK;
+    KvCopyArgs a = {};
+    a.pages = static_cast<unsigned char *>(kv->pages);
+    a.page_bytes = (long long)bytes;
+    a.layer_bytes = (long long)layer_bytes;
+    a.n_pages = kv->n_pages;
+    a.src = src;
+    a.dst = dst;
+    a.err = kv->err;
+    // 16 KB per CTA (256 threads x 4 loads of 16 bytes) until the pages are covered
+    const unsigned per_page = (unsigned)std::max<size_t>(1, (bytes + 16383) / 16384);
+    return launch(kv_copy_kernel, dim3((unsigned)n, per_page, (unsigned)layers), 256, 0, a, stream);
+}
+
+size_t zt_q4_kv_attention_workspace_bytes(int kv_heads, int q_heads, int head_dim, int tokens)
+{
+    if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 16384 || tokens < 1 || tokens > 16) return 0;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128) return 0;
+    return part_bytes(head_dim, 8 * column_tiles(q_heads / kv_heads * tokens));
+}
+
+int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, int q_heads, int tokens, const int32_t *lens,
+                       const int32_t *page_table, int n_seqs, int max_pages, float scale, uint16_t *out, int ld_out,
+                       void *workspace, size_t ws_bytes, void *stream)
+{
+    int rc = check_kv(kv);
+    if (!rc) rc = check_table(page_table, n_seqs, max_pages, kv->page_size);
+    if (rc) return rc;
+    if (!lens || !out || !workspace || n_seqs > ZT_Q4_KV_MAX_SEQS || tokens < 1 || tokens > 16) return ZT_ERR_INVALID_ARG;
+    if (q_heads < kv->kv_heads || q_heads % kv->kv_heads || q_heads > 16384) return ZT_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return ZT_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)q_heads * kv->head_dim;
+    if ((rc = check_matrix(q, ld_q, width))) return rc;
+    if (ld_out < width) return ZT_ERR_INVALID_ARG;
+    if (!aligned(out, 2) || !aligned(lens, 4) || !aligned(workspace, 16)) return ZT_ERR_MISALIGNED;
+    if (ws_bytes < zt_q4_kv_attention_workspace_bytes(kv->kv_heads, q_heads, kv->head_dim, tokens)) return ZT_ERR_WORKSPACE;
+    KvAttnArgs a = {};
+    a.at = places(kv, page_table, n_seqs, max_pages);
+    a.q = h(q);
+    a.out = h(out);
+    a.lens = lens;
+    a.part = static_cast<float *>(workspace);
+    a.ld_q = ld_q;
+    a.ld_out = ld_out;
+    a.tokens = tokens;
+    a.q_heads = q_heads;
+    a.group = q_heads / kv->kv_heads;
+    a.cols = a.group * tokens;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    if (kv->head_dim == 64) return launch_attention<64>(a, stream);
+    if (kv->head_dim == 96) return launch_attention<96>(a, stream);
+    return launch_attention<128>(a, stream);
+}
+
+int zt_q4_kv_errors(const uint32_t *err, unsigned int *out)
+{
+    if (!err || !out) return ZT_ERR_INVALID_ARG;
+    const cudaError_t e = cudaMemcpy(out, err, sizeof(unsigned int), cudaMemcpyDeviceToHost);
+    return e == cudaSuccess ? ZT_OK : device_error(e, ZT_ERR_DEVICE);
+}
+
+}  // extern "C"

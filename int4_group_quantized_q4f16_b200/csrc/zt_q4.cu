@@ -4,7 +4,6 @@
 // Host side only: argument checks, launch-shape selection and launches.  Every
 // check runs before the first CUDA call, so a rejected call launches nothing.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -14,6 +13,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "zt_host.h"
 #include "q4_common.cuh"
 #include "q4_mma.cuh"
 #include "q4_pass.cuh"
@@ -24,8 +24,6 @@ namespace {
 
 using namespace zt;
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 int check_shapes(int M, int N, int K, int row_mult)
 {
     if (M < 1 || M > 16 || N < 1 || K < kGroup || K % kGroup) return ZT_ERR_INVALID_ARG;
@@ -33,93 +31,6 @@ int check_shapes(int M, int N, int K, int row_mult)
     return ZT_OK;
 }
 
-struct OccKey {
-    const void *fn;
-    int dev, threads;
-    size_t smem;
-    bool operator==(const OccKey &o) const
-    {
-        return fn == o.fn && dev == o.dev && threads == o.threads && smem == o.smem;
-    }
-};
-struct OccHash {
-    size_t operator()(const OccKey &k) const
-    {
-        return std::hash<const void *>()(k.fn) ^ (size_t)k.dev * 131 ^ (size_t)k.threads * 7919 ^
-               k.smem * 104729;
-    }
-};
-
-// last CUDA error seen by a library call on this host thread (diagnostics only)
-thread_local cudaError_t g_last_cuda_error = cudaSuccess;
-
-// Launch status: clear a stale non-sticky error left by an earlier, unrelated
-// runtime call before launching (so it is not blamed on this launch), then
-// read and clear the launch's own error.
-void clear_stale_error() { (void)cudaGetLastError(); }
-
-int launch_status()
-{
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) return ZT_OK;
-    g_last_cuda_error = e;
-    return ZT_ERR_LAUNCH;
-}
-
-std::mutex g_mu;
-std::unordered_map<OccKey, int, OccHash> g_occ;   // resident CTAs per SM, or -1 if unusable
-std::unordered_map<int, int> g_sms;               // device -> SM count
-
-std::unordered_map<uint64_t, bool> g_optin;      // (kernel, device) opted in to the max smem
-
-// Resident CTAs per SM for (kernel, block, smem) on the current device.  On
-// first use of a kernel on a device its dynamic shared memory limit is raised
-// once to the device's opt-in maximum, so every later launch of any size fits.
-int resident_ctas(const void *fn, int threads, size_t smem, int &sms)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) {
-        g_last_cuda_error = e;
-        return -1;
-    }
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it_s = g_sms.find(dev);
-    if (it_s == g_sms.end()) {
-        int n = 0;
-        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess || n < 1) {
-            g_last_cuda_error = e;
-            return -1;
-        }
-        it_s = g_sms.emplace(dev, n).first;
-    }
-    sms = it_s->second;
-    const uint64_t fkey = (uint64_t)(uintptr_t)fn * 64u + (uint64_t)dev;
-    if (g_optin.find(fkey) == g_optin.end()) {
-        int optin = 0;
-        e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
-        if (e != cudaSuccess) {
-            g_last_cuda_error = e;
-            (void)cudaGetLastError();
-            return -1;
-        }
-        g_optin.emplace(fkey, true);
-    }
-    OccKey key{fn, dev, threads, smem};
-    auto it = g_occ.find(key);
-    if (it != g_occ.end()) return it->second;
-    int nb = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, threads, smem);
-    if (e != cudaSuccess) {
-        g_last_cuda_error = e;
-        (void)cudaGetLastError();
-        return -1;
-    }
-    g_occ.emplace(key, nb > 0 ? nb : -1);
-    return nb > 0 ? nb : -1;
-}
 
 // shared memory per CTA for 2 and for 1 resident CTA per SM (228 KiB per SM,
 // 1 KiB reserved per CTA)
@@ -340,6 +251,7 @@ size_t lmhead_ws_bytes(int M) { return (size_t)kMaxCtas * M * (sizeof(float) + s
 // of the library.  Sized for the largest LM-head workspace (M = 16).
 constexpr size_t kNoAllocScratchBytes = (size_t)kMaxCtas * 16 * (sizeof(float) + sizeof(int));   // 512 KiB
 __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratchBytes];
+std::mutex g_mu;
 std::unordered_map<int, void *> g_noalloc_ptr;   // device -> device address of g_noalloc_scratch
 
 // Device address of the scratch array on the current device, looked up once
@@ -368,22 +280,6 @@ void *noalloc_scratch()
 }
 
 // ------------------------------------------------ batched (prefill) GEMM ----
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the
-// driver library needed).
-PFN_cuTensorMapEncodeTiled_v12000 tma_encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        (void)cudaGetLastError();
-    });
-    return fn;
-}
 
 // fp16 [rows][K] row-major, boxes of 64 k x box_rows rows, 128-byte swizzle,
 // out-of-range elements read as zero.
@@ -603,7 +499,7 @@ int read_error_word(const void *p, unsigned int *out)
 
 extern "C" {
 
-int zt_q4_version(void) { return (1 << 16) | 6; }
+int zt_q4_version(void) { return (1 << 16) | 7; }
 
 const char *zt_q4_last_cuda_error(void)
 {

@@ -64,6 +64,25 @@ class ZtProj(ctypes.Structure):
                 ("group", ctypes.c_int), ("norm", ctypes.POINTER(ZtNorm)), ("rope", ctypes.POINTER(ZtRope))]
 
 
+class ZtKv(ctypes.Structure):
+    """struct zt_q4_kv of include/zt_q4.h (a paged 4-bit KV cache)"""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("err", ctypes.c_void_p)]
+
+
+class ZtKvRows(ctypes.Structure):
+    """struct zt_q4_kv_rows of include/zt_q4.h (places of appended or gathered rows)"""
+    _fields_ = [("seq", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("n", ctypes.c_int),
+                ("page_table", ctypes.c_void_p), ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class ZtKvRope(ctypes.Structure):
+    """struct zt_q4_kv_rope of include/zt_q4.h (rotary embedding of an append)"""
+    _fields_ = [("theta", ctypes.c_float), ("q", ctypes.c_void_p), ("ld_q", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("q_out", ctypes.c_void_p), ("ld_q_out", ctypes.c_int), ("k_out", ctypes.c_void_p),
+                ("ld_k_out", ctypes.c_int)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -114,6 +133,20 @@ def _load() -> ctypes.CDLL:
     lib.zt_q4_version.argtypes = []
     lib.zt_q4_last_cuda_error.argtypes = []
     lib.zt_q4_last_cuda_error.restype = ctypes.c_char_p
+    lib.zt_q4_kv_page_bytes.argtypes = [_I, _I, _I]
+    lib.zt_q4_kv_page_bytes.restype = ctypes.c_size_t
+    lib.zt_q4_kv_append.argtypes = [ctypes.POINTER(ZtKv), ctypes.POINTER(ZtKvRows), _P, _I, _P, _I,
+                                    ctypes.POINTER(ZtKvRope), _P]
+    lib.zt_q4_kv_gather.argtypes = [ctypes.POINTER(ZtKv), ctypes.POINTER(ZtKvRows), _P, _I, _P, _I, _P]
+    lib.zt_q4_kv_copy_pages.argtypes = [ctypes.POINTER(ZtKv), _P, _P, _I, _I, ctypes.c_size_t, _P]
+    lib.zt_q4_kv_attention_workspace_bytes.argtypes = [_I, _I, _I, _I]
+    lib.zt_q4_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.zt_q4_kv_attention.argtypes = [ctypes.POINTER(ZtKv), _P, _I, _I, _I, _P, _P, _I, _I, ctypes.c_float, _P, _I,
+                                       _P, ctypes.c_size_t, _P]
+    lib.zt_q4_kv_errors.argtypes = [_P, ctypes.POINTER(ctypes.c_uint)]
+    for f in (lib.zt_q4_kv_append, lib.zt_q4_kv_gather, lib.zt_q4_kv_copy_pages, lib.zt_q4_kv_attention,
+              lib.zt_q4_kv_errors):
+        f.restype = ctypes.c_int
     for f in (lib.zt_q4_gemv, lib.zt_q4_gate_up_silu, lib.zt_q4_lmhead_argmax,
               lib.zt_q4_pack_host, lib.zt_q4_unpack_host, lib.zt_q4_version):
         f.restype = ctypes.c_int
@@ -466,3 +499,221 @@ class Pass:
         v = ctypes.c_uint(0)
         _check(lib.zt_q4_pass_errors(self.workspace.data_ptr(), self.n, ctypes.byref(v)), "zt_q4_pass_errors")
         return int(v.value)
+
+
+# ----------------------------------------------- paged 4-bit KV cache --
+ZT_Q4_KV_ERR_PLACE = 1
+ZT_Q4_KV_ERR_WAIT = 2
+ZT_Q4_KV_MAX_SEQS = 4096
+
+
+def kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of the 4-bit cache (one layer)."""
+    n = int(lib.zt_q4_kv_page_bytes(page_size, kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(f"no cache page of {page_size} tokens, {kv_heads} heads of {head_dim}: page_size is a multiple "
+                         "of 16 up to 1024, head_dim 64, 96 or 128")
+    return n
+
+
+def kv_attention_workspace_bytes(kv_heads: int, q_heads: int, head_dim: int, tokens: int = 1) -> int:
+    return int(lib.zt_q4_kv_attention_workspace_bytes(kv_heads, q_heads, head_dim, tokens))
+
+
+def _on(t, device, dtype, what, dim):
+    if not t.is_cuda or t.device != device or t.dtype != dtype or t.dim() != dim:
+        raise ValueError(f"{what} must be a {dim}-D {dtype} CUDA tensor on {device}")
+
+
+def _ints(t, device, what, dim=1, numel=None):
+    torch = _torch()
+    _on(t, device, torch.int32, what, dim)
+    if not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{what} must be contiguous" + (f" with {numel} elements" if numel is not None else ""))
+    return t.data_ptr()
+
+
+def _heads(t, device, what, rows, heads, dim):
+    """(pointer, row stride) of fp16 rows [rows][heads][dim] whose heads lie side by side."""
+    torch = _torch()
+    _on(t, device, torch.float16, what, 3)
+    if rows is None:
+        rows = t.shape[0]
+    if tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{what} must be [{rows}, {heads}, {dim}], is {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or (rows > 1 and t.stride(0) < heads * dim):
+        raise ValueError(f"the heads of a row of {what} must lie side by side, rows behind each other")
+    return t.data_ptr(), int(t.stride(0)) if rows > 1 else heads * dim
+
+
+class _Launch:
+    """A call whose arguments are checked and marshalled once; run() only launches, on the tensors' device and its
+    current stream (or `stream`).  The tensors are kept alive; their contents are read at run()."""
+
+    def __init__(self, name, device, args, keep, result):
+        self._fn, self._name, self._args, self._keep, self._result = getattr(lib, name), name, args, keep, result
+        self._device = device
+
+    def _launch(self, stream):
+        torch = _torch()
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device).cuda_stream
+        else:
+            stream = _stream_handle(stream)
+        _check(self._fn(*self._args, stream), self._name)
+
+    def run(self, stream=None):
+        torch = _torch()
+        if torch.cuda.current_device() == self._device.index:
+            self._launch(stream)
+        else:
+            with torch.cuda.device(self._device):
+                self._launch(stream)
+        return self._result
+
+
+class KvCache:
+    """A paged 4-bit KV cache (layout and quantization: include/zt_q4.h) over `pages`, a uint8 CUDA tensor
+    [layers, n_pages, page_bytes] (or [n_pages, page_bytes] for one layer) that the caller owns.  A device error word
+    collects indices out of range; errors() reads it (synchronous), clear_errors() resets it."""
+
+    def __init__(self, pages, page_size: int, kv_heads: int, head_dim: int):
+        torch = _torch()
+        nbytes = kv_page_bytes(page_size, kv_heads, head_dim)
+        if pages.dim() == 2:
+            pages = pages.unsqueeze(0)
+        if not pages.is_cuda or pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
+            raise ValueError("pages must be a contiguous uint8 CUDA tensor [layers, n_pages, page_bytes]")
+        if pages.shape[2] != nbytes or pages.shape[0] < 1 or pages.shape[1] < 1:
+            raise ValueError(f"a page of {page_size} tokens has {nbytes} bytes, pages is {tuple(pages.shape)}")
+        self.pages, self.device = pages, pages.device
+        self.layers, self.n_pages, self.page_bytes = (int(n) for n in pages.shape)
+        self.page_size, self.kv_heads, self.head_dim = page_size, kv_heads, head_dim
+        self.err = torch.zeros((1,), dtype=torch.int32, device=self.device)
+
+    @classmethod
+    def empty(cls, layers: int, n_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        """A cache on memory of its own (zeros: every place reads back as 0)."""
+        torch = _torch()
+        return cls(torch.zeros((layers, n_pages, kv_page_bytes(page_size, kv_heads, head_dim)), dtype=torch.uint8,
+                               device=device), page_size, kv_heads, head_dim)
+
+    def _struct(self, layer: int) -> ZtKv:
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of a cache of {self.layers}")
+        return ZtKv(self.pages.data_ptr() + layer * self.n_pages * self.page_bytes, self.n_pages, self.page_size,
+                    self.kv_heads, self.head_dim, self.err.data_ptr())
+
+    def _rows(self, seq, pos, table) -> ZtKvRows:
+        n = int(pos.numel())
+        return ZtKvRows(_ints(seq, self.device, "seq", 1, n), _ints(pos, self.device, "pos", 1, n), n,
+                        _ints(table, self.device, "table", 2), int(table.shape[0]), int(table.shape[1]))
+
+    def errors(self) -> int:
+        v = ctypes.c_uint(0)
+        _check(lib.zt_q4_kv_errors(self.err.data_ptr(), ctypes.byref(v)), "zt_q4_kv_errors")
+        return int(v.value)
+
+    def clear_errors(self) -> None:
+        self.err.zero_()
+
+
+class KvAppend(_Launch):
+    """Appends rows to layer `layer` of a cache: k and v fp16 [n, kv_heads, head_dim] (rows may be strided: views into
+    a QKV buffer) go to positions pos of sequences seq (int32 [n]; pos < 0 skips the row) through the page table
+    int32 [n_seqs, max_pages].  With theta, k and q (fp16 [n, q_heads, head_dim], optional) are rotated first;
+    run() returns (rotated q or None, rotated k), written to q_out and k_out (allocated here when not given)."""
+
+    def __init__(self, cache: KvCache, k, v, seq, pos, table, layer: int = 0, q=None, theta=None, q_out=None, k_out=None):
+        torch = _torch()
+        n, dev, dim = int(pos.numel()), cache.device, cache.head_dim
+        kv, rows = cache._struct(layer), cache._rows(seq, pos, table)
+        kp, ld_k = _heads(k, dev, "k", n, cache.kv_heads, dim)
+        vp, ld_v = _heads(v, dev, "v", n, cache.kv_heads, dim)
+        rope = None
+        if theta is None:
+            if q is not None or q_out is not None or k_out is not None:
+                raise ValueError("q, q_out and k_out belong to a rotation: give theta")
+        else:
+            if q is None and q_out is not None:
+                raise ValueError("q_out without q")
+            if k_out is None:
+                k_out = torch.empty((n, cache.kv_heads, dim), dtype=torch.float16, device=dev)
+            rope = ZtKvRope(float(theta))
+            rope.k_out, rope.ld_k_out = _heads(k_out, dev, "k_out", n, cache.kv_heads, dim)
+            if q is not None:
+                rope.q_heads = int(q.shape[1]) if q.dim() == 3 else 0
+                if q_out is None:
+                    q_out = torch.empty((n, rope.q_heads, dim), dtype=torch.float16, device=dev)
+                rope.q, rope.ld_q = _heads(q, dev, "q", n, rope.q_heads, dim)
+                rope.q_out, rope.ld_q_out = _heads(q_out, dev, "q_out", n, rope.q_heads, dim)
+        super().__init__("zt_q4_kv_append", dev,
+                         (ctypes.byref(kv), ctypes.byref(rows), kp, ld_k, vp, ld_v,
+                          ctypes.byref(rope) if rope else None),
+                         (cache, k, v, seq, pos, table, q, q_out, k_out, kv, rows, rope), (q_out, k_out))
+
+
+class KvGather(_Launch):
+    """Reads rows of a cache back as fp16: run() returns (k, v) [n, kv_heads, head_dim], row i being position pos[i] of
+    sequence seq[i] (pos < 0 leaves the row as it was)."""
+
+    def __init__(self, cache: KvCache, seq, pos, table, layer: int = 0, k=None, v=None):
+        torch = _torch()
+        n, dev, dim = int(pos.numel()), cache.device, cache.head_dim
+        kv, rows = cache._struct(layer), cache._rows(seq, pos, table)
+        k = torch.empty((n, cache.kv_heads, dim), dtype=torch.float16, device=dev) if k is None else k
+        v = torch.empty((n, cache.kv_heads, dim), dtype=torch.float16, device=dev) if v is None else v
+        kp, ld_k = _heads(k, dev, "k", n, cache.kv_heads, dim)
+        vp, ld_v = _heads(v, dev, "v", n, cache.kv_heads, dim)
+        super().__init__("zt_q4_kv_gather", dev, (ctypes.byref(kv), ctypes.byref(rows), kp, ld_k, vp, ld_v),
+                         (cache, seq, pos, table, k, v, kv, rows), (k, v))
+
+
+class KvCopy(_Launch):
+    """Copies page src[i] onto page dst[i] (int32 CUDA tensors) in every layer of a cache.  No page may be both a
+    destination and another entry's source or destination."""
+
+    def __init__(self, cache: KvCache, src, dst):
+        n = int(src.numel())
+        kv = cache._struct(0)
+        super().__init__("zt_q4_kv_copy_pages", cache.device,
+                         (ctypes.byref(kv), _ints(src, cache.device, "src", 1, n), _ints(dst, cache.device, "dst", 1, n), n,
+                          cache.layers, cache.n_pages * cache.page_bytes), (cache, src, dst, kv), cache.pages)
+
+
+class KvAttention(_Launch):
+    """Attention of the last tokens of each sequence over a cache that already holds them: q fp16
+    [n_seqs, tokens, q_heads, head_dim] (tokens 1..16, rows may be strided), lens int32 [n_seqs] (cached tokens),
+    table int32 [n_seqs, max_pages].  run() returns out, like q and contiguous when not given; a query that sees no
+    token gets zeros.  scale defaults to head_dim ** -0.5.  Calls that may overlap need workspaces of their own."""
+
+    def __init__(self, cache: KvCache, q, lens, table, layer: int = 0, out=None, scale=None, workspace=None):
+        torch = _torch()
+        dev, dim = cache.device, cache.head_dim
+        _on(q, dev, torch.float16, "q", 4)
+        seqs, tokens, heads = (int(n) for n in q.shape[:3])
+        kv = cache._struct(layer)
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+        (qp, ld_q), (op, ld_out) = (self._rows_of(t, dev, what, seqs, tokens, heads, dim)
+                                    for t, what in ((q, "q"), (out, "out")))
+        if int(table.shape[0]) != seqs:
+            raise ValueError(f"table has {table.shape[0]} rows for {seqs} sequences")
+        nbytes = kv_attention_workspace_bytes(cache.kv_heads, heads, dim, tokens)
+        if workspace is None:
+            workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        super().__init__("zt_q4_kv_attention", dev,
+                         (ctypes.byref(kv), qp, ld_q, heads, tokens, _ints(lens, dev, "lens", 1, seqs),
+                          _ints(table, dev, "table", 2), seqs, int(table.shape[1]),
+                          float(dim ** -0.5 if scale is None else scale), op, ld_out, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size()),
+                         (cache, q, lens, table, out, workspace, kv), out)
+
+    @staticmethod
+    def _rows_of(t, dev, what, seqs, tokens, heads, dim):
+        _on(t, dev, _torch().float16, what, 4)
+        if tokens > 1 and seqs > 1 and t.stride(0) != tokens * t.stride(1):
+            raise ValueError(f"the tokens of {what} must lie at one stride")
+        row = t.stride(1) if tokens > 1 else t.stride(0)
+        flat = t.as_strided((seqs * tokens, t.shape[2], t.shape[3]), (row, t.stride(2), t.stride(3)), t.storage_offset())
+        return _heads(flat, dev, what, seqs * tokens, heads, dim)

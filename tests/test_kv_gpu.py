@@ -1,0 +1,378 @@
+"""GPU parity of the paged 4-bit KV cache (append with rotary embedding, gather, page copies) and of attention over it,
+against float64 (kv_reference.py).
+
+Tolerances.  Codes and scales are bit-exact: x / s of fp16 values is a half-integer exactly or at least 2^-13 (relative)
+away from one, and -min / 7 at least 2^-15 away from an fp16 rounding boundary, both far above an fp32 rounding.
+A gathered value is the exact product rounded once to fp16.  A rotated value: cos and sin rounded to fp32, two products and
+a sum rounded in fp32 stay within 2^-22 (|x| + |y|), then half an fp16 step.
+Attention: the weights are rounded to fp16 before and after V's scale (2^-11 each: 2^-10 of sum w |v|); scores carry an
+absolute error e from their fp32 arithmetic, (D / 32 + 2) 2^-24 times sum |q (code) s| and 2^-24 |s| (in the exponent's
+units, here below 64), which moves weights by 2 e ln 2 < 2^-14: together (2^-10 + 2^-14) sum w |v|.  Products
+weight * V scale below fp16's normal range are off by up to 2^-25, times |code - 7| <= 8, with the largest weight at 2^12 or
+more (at 1 or more from the first V scale of 2 on): 2^-34 (2^-22) a token; weights themselves there by 2^-37 (2^-25) of |v|.
+Then half an fp16 step of the result (2^-11, or 2^-25 for subnormals)."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def zt():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from int4_group_quantized_q4f16_b200 import zt_q4
+    return zt_q4
+
+
+def cuda(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def fp16(rng, *shape, by=1.0):
+    return (rng.standard_normal(shape) * by).astype(np.float16)
+
+
+def same_bytes(cache, pool):
+    got = cache.pages[0].cpu().numpy().reshape(pool.raw.shape)
+    bad = np.argwhere(got != pool.raw)
+    assert not len(bad), f"{len(bad)} bytes differ, first at (page, head, tile, byte) {bad[:5].tolist()}: " \
+                         f"{[(int(got[tuple(i)]), int(pool.raw[tuple(i)])) for i in bad[:5]]}"
+
+
+def tables(rng, lens, page, spare=2):
+    """A page table in random order and the number of pages; entries behind a sequence's pages are out of range."""
+    width = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(width) + spare)
+    table = np.full((len(lens), max(max(width), 1)), 2**31 - 1, np.int32)
+    at = 0
+    for b, w in enumerate(width):
+        table[b, :w] = order[at:at + w]
+        at += w
+    return table, sum(width) + spare
+
+
+def filled(zt, rng, lens, page, heads, D, k_by=1.0, v_by=1.0, edit=None):
+    """A cache holding random rows, written by the reference into random bytes."""
+    table, n = tables(rng, lens, page)
+    raw = rng.integers(0, 256, (n, zt.kv_page_bytes(page, heads, D)), dtype=np.uint8)
+    pool = ref.Pool(raw, page, heads, D)
+    for b, m in enumerate(lens):
+        for p in range(m):
+            k, v = fp16(rng, heads, D, by=k_by), fp16(rng, heads, D, by=v_by)
+            if edit:
+                edit(b, p, k, v)
+            pool.write(table[b, p // page], p % page, k, v)
+    return zt.KvCache(cuda(raw), page, heads, D), pool, table
+
+
+def check_attention(zt, cache, pool, q, lens, table, scale=None, large_v=False, **more):
+    import torch
+    tokens, D = q.shape[1], q.shape[3]
+    plan = zt.KvAttention(cache, cuda(q), cuda(np.asarray(lens, np.int32)), cuda(table), scale=scale, **more)
+    got = plan.run().cpu().numpy()
+    again = plan.run().clone()
+    torch.cuda.synchronize()
+    assert cache.errors() == 0
+    assert np.array_equal(again.cpu().numpy().view(np.uint16), got.view(np.uint16)), "two runs differ"
+    for b, n in enumerate(lens):
+        k, v = pool.values(table[b, :-(-n // pool.page)], n)
+        with np.errstate(all="ignore"):
+            want, mag = ref.attention(q[b], k, v, [n - tokens + 1 + i for i in range(tokens)], scale or D ** -0.5)
+        top = np.nanmax(np.abs(v), initial=0.0)
+        tol = (2.0**-10 + 2.0**-14) * mag + 2.0**-11 * np.abs(want) + 2.0**-25 + n * 2.0**(0 if large_v else -12) * (2.0**-22 + 2.0**-25 * top)
+        assert np.array_equal(np.isnan(got[b]), np.isnan(want)), f"sequence {b}: NaN in other places"
+        fine = ~np.isnan(want)
+        err = np.abs(got[b].astype(np.float64) - want)
+        assert (err <= tol)[fine].all(), (b, n, float((err - tol)[fine].max()), float(err[fine].max()))
+    return got
+
+
+# ------------------------------------------------------------- append, gather --
+@pytest.mark.parametrize("D,heads,page", [(64, 3, 16), (96, 32, 64), (128, 8, 32), (128, 1, 1024)])
+def test_append_is_bit_exact_and_gathers_back(zt, D, heads, page):
+    rng = np.random.default_rng(D + heads)
+    lens = [1, 16, 37, 2 * page + 5 if page < 100 else 40, 0, 8]
+    table, n = tables(rng, lens, page)
+    raw = rng.integers(0, 256, (n, zt.kv_page_bytes(page, heads, D)), dtype=np.uint8)
+    want = ref.Pool(raw.copy(), page, heads, D)
+    cache = zt.KvCache(cuda(raw), page, heads, D)
+    places = [(b, p) for b, m in enumerate(lens) for p in range(m)]
+    rng.shuffle(places)
+    places = places[:-7] + [(0, -1), (99, -1)] + places[-7:]            # padding rows, and a second call
+    rows = len(places)
+    # values of every kind: zeros, ties, one-sided groups, subnormals, the largest
+    x = fp16(rng, rows, 2 * heads + 1, D)
+    x[1] = 0
+    x[2] = np.float16(-1.5)
+    x[3] = np.abs(x[3])
+    x[4] *= np.float16(6e-8)
+    x[5] = np.float16(65504) * np.sign(x[5])
+    x[6] = np.rint(x[6] * 4) / 4
+    x[7, :, :32] = np.inf
+    x[8, :, 33] = np.nan
+    seq, pos = (np.array(c, np.int32) for c in zip(*places))
+    dev, (sd, pd, td) = cuda(x), (cuda(a) for a in (seq, pos, table))
+    for part in (slice(0, rows - 7), slice(rows - 7, rows)):
+        zt.KvAppend(cache, dev[part, :heads], dev[part, heads:2 * heads], sd[part], pd[part], td).run()
+    for i, (b, p) in enumerate(places):
+        if p >= 0:
+            want.write(table[b, p // page], p % page, x[i, :heads], x[i, heads:2 * heads])
+    same_bytes(cache, want)
+    k, v = zt.KvGather(cache, sd, pd, td, k=cuda(np.full((rows, heads, D), 9, np.float16))).run()
+    k, v = k.cpu().numpy(), v.cpu().numpy()
+    assert cache.errors() == 0
+    for i, (b, p) in enumerate(places):
+        if p < 0:
+            assert (k[i] == 9).all()
+            continue
+        wk, wv = (ref.dequantize(*ref.quantize(y)).astype(np.float16) for y in (x[i, :heads], x[i, heads:2 * heads]))
+        assert np.array_equal(k[i], wk, equal_nan=True) and np.array_equal(v[i], wv, equal_nan=True), i
+
+
+@pytest.mark.parametrize("D,heads,q_heads", [(64, 2, 6), (96, 32, 32), (128, 8, 32)])
+def test_append_rotates(zt, D, heads, q_heads):
+    rng = np.random.default_rng(D)
+    rows, page, theta = 21, 16, 10000.0
+    pos = np.array([0, 1, 2, 131071, 2**20 + 3] + list(range(100, 100 + rows - 5)), np.int32)
+    # every row a sequence of its own whose table points the pages it needs at one page
+    table = np.repeat(np.arange(rows, dtype=np.int32)[:, None], int(pos.max()) // page + 1, 1)
+    raw = rng.integers(0, 256, (rows, zt.kv_page_bytes(page, heads, D)), dtype=np.uint8)
+    want = ref.Pool(raw.copy(), page, heads, D)
+    cache = zt.KvCache(cuda(raw), page, heads, D)
+    x = fp16(rng, rows, q_heads + 2 * heads, D)
+    dev = cuda(x)
+    q, k = zt.KvAppend(cache, dev[:, q_heads:q_heads + heads], dev[:, q_heads + heads:], cuda(np.arange(rows, dtype=np.int32)),
+                       cuda(pos), cuda(table), q=dev[:, :q_heads], theta=theta).run()
+    q, k = q.cpu().numpy(), k.cpu().numpy()
+    assert cache.errors() == 0
+    half = D // 2
+    for got, src in ((q, x[:, :q_heads]), (k, x[:, q_heads:q_heads + heads])):
+        exact = ref.rotate(src, pos, theta)
+        mag = np.abs(src.astype(np.float64))
+        mag = mag + np.concatenate([mag[..., half:], mag[..., :half]], -1)
+        assert (np.abs(got - exact) <= 2.0**-11 * np.abs(exact) + 2.0**-25 + 2.0**-22 * mag).all()
+    assert np.array_equal(q[0], x[0, :q_heads]) and np.array_equal(k[0], x[0, q_heads:q_heads + heads])   # position 0
+    for i in range(rows):
+        want.write(i, pos[i] % page, k[i], x[i, q_heads + heads:])
+    same_bytes(cache, want)
+
+
+def test_append_reports_places_out_of_range(zt):
+    """Bad pages, positions and sequences set the error bit and write nothing; the other rows are stored."""
+    rng = np.random.default_rng(5)
+    page, heads, D = 16, 2, 64
+    table = np.array([[1, -1], [7, 0]], np.int32)              # -1 and 7 are not pages of a pool of 4
+    raw = rng.integers(0, 256, (4, zt.kv_page_bytes(page, heads, D)), dtype=np.uint8)
+    want = ref.Pool(raw.copy(), page, heads, D)
+    cache = zt.KvCache(cuda(raw), page, heads, D)
+    seq = np.array([0, 0, 1, 1, 0, 2, -1], np.int32)
+    pos = np.array([3, 16, 0, 17, 32, 0, 0], np.int32)
+    k, v = fp16(rng, 7, heads, D), fp16(rng, 7, heads, D)
+    args = cuda(seq), cuda(pos), cuda(table)
+    zt.KvAppend(cache, cuda(k), cuda(v), *args).run()
+    assert cache.errors() == zt.ZT_Q4_KV_ERR_PLACE
+    want.write(1, 3, k[0], v[0])
+    want.write(0, 1, k[3], v[3])
+    same_bytes(cache, want)
+    cache.clear_errors()
+    assert cache.errors() == 0
+    gk, _ = zt.KvGather(cache, *args, k=cuda(np.full((7, heads, D), 9, np.float16))).run()
+    assert cache.errors() == zt.ZT_Q4_KV_ERR_PLACE
+    assert [(gk[i] == 9).all().item() for i in range(7)] == [False, True, True, False, True, True, True]
+
+
+def test_offsets_beyond_32_bits(zt):
+    """Pages behind the first 4 GiB of a pool: append, gather, attention and copies reach them."""
+    import torch
+    page, heads, D = 1024, 32, 128
+    size = zt.kv_page_bytes(page, heads, D)
+    n = (5 << 30) // size
+    cache = zt.KvCache(torch.zeros((n, size), dtype=torch.uint8, device="cuda"), page, heads, D)
+    rng = np.random.default_rng(1)
+    k, v = fp16(rng, 3, heads, D), fp16(rng, 3, heads, D)
+    table = cuda(np.array([[n - 1], [n - 2]], np.int32))
+    seq, pos = cuda(np.zeros(3, np.int32)), cuda(np.array([0, 1, 2], np.int32))
+    zt.KvAppend(cache, cuda(k), cuda(v), seq, pos, table).run()
+    zt.KvCopy(cache, cuda(np.array([n - 1], np.int32)), cuda(np.array([n - 2], np.int32))).run()
+    for b in (0, 1):
+        gk, gv = zt.KvGather(cache, seq + b, pos, table).run()
+        assert np.array_equal(gk.cpu().numpy(), ref.dequantize(*ref.quantize(k)).astype(np.float16))
+        assert np.array_equal(gv.cpu().numpy(), ref.dequantize(*ref.quantize(v)).astype(np.float16))
+    q = cuda(fp16(rng, 2, 1, heads, D))
+    q[1] = q[0]
+    out = zt.KvAttention(cache, q, cuda(np.array([3, 3], np.int32)), table).run()
+    torch.cuda.synchronize()
+    assert cache.errors() == 0 and out.abs().sum() > 0
+    assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_copy_pages(zt, layers):
+    import torch
+    rng = np.random.default_rng(layers)
+    page, heads, D, n = 48, 3, 96, 11
+    raw = rng.integers(0, 256, (layers, n, zt.kv_page_bytes(page, heads, D)), dtype=np.uint8)
+    cache = zt.KvCache(cuda(raw), page, heads, D)
+    src, dst = np.array([3, 3, 10, 5, 8], np.int32), np.array([0, 1, 2, 5, 9], np.int32)
+    zt.KvCopy(cache, cuda(src), cuda(dst)).run()
+    raw[:, dst] = raw[:, src]
+    assert np.array_equal(cache.pages.cpu().numpy(), raw) and cache.errors() == 0
+    zt.KvCopy(cache, cuda(np.array([n, 2, -1, 4], np.int32)), cuda(np.array([0, n, 1, 6], np.int32))).run()
+    raw[:, 6] = raw[:, 4]
+    assert np.array_equal(cache.pages.cpu().numpy(), raw) and cache.errors() == zt.ZT_Q4_KV_ERR_PLACE
+    zt.KvCopy(cache, torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")).run()
+
+
+# ------------------------------------------------------------------ attention --
+LENS = [0, 1, 15, 16, 17, 33, 100, 257]
+
+
+@pytest.mark.parametrize("D,q_heads,heads,tokens,page", [
+    (64, 4, 4, 1, 16), (96, 4, 4, 1, 64), (128, 8, 2, 1, 32), (128, 5, 1, 1, 16), (64, 16, 2, 1, 48), (96, 9, 1, 1, 16),
+    (128, 16, 1, 1, 16), (128, 17, 1, 1, 16), (64, 2, 2, 4, 16), (96, 6, 2, 3, 32), (128, 4, 2, 16, 16), (64, 40, 2, 1, 16)])
+def test_attention(zt, D, q_heads, heads, tokens, page):
+    rng = np.random.default_rng(D * 100 + q_heads * 10 + tokens)
+    cache, pool, table = filled(zt, rng, LENS, page, heads, D)
+    check_attention(zt, cache, pool, fp16(rng, len(LENS), tokens, q_heads, D, by=2.0), LENS, table)
+
+
+@pytest.mark.parametrize("D,q_heads,heads", [(128, 4, 1), (96, 2, 2), (64, 3, 1)])
+def test_attention_long_sequences(zt, D, q_heads, heads):
+    """Sequences cut between many CTAs, next to short ones."""
+    rng = np.random.default_rng(D)
+    lens = [5, 7001, 0, 1300, 1]
+    cache, pool, table = filled(zt, rng, lens, 64, heads, D)
+    check_attention(zt, cache, pool, fp16(rng, len(lens), 1, q_heads, D, by=2.0), lens, table)
+
+
+def test_attention_many_sequences(zt):
+    """More sequences than one warp's prefix sum, most of them a single token or none."""
+    rng = np.random.default_rng(3)
+    lens = [int(n) for n in rng.integers(0, 4, 300)]
+    lens[123] = 90
+    cache, pool, table = filled(zt, rng, lens, 16, 1, 64)
+    check_attention(zt, cache, pool, fp16(rng, len(lens), 1, 2, 64), lens, table)
+
+
+def test_attention_scale_and_strides(zt):
+    """q as the first heads of a QKV buffer, out as rows of a wider one, a scale of the caller's."""
+    import torch
+    rng = np.random.default_rng(4)
+    lens, D = [40, 3], 96
+    cache, pool, table = filled(zt, rng, lens, 16, 2, D)
+    q = fp16(rng, 2, 1, 4, D)
+    got = check_attention(zt, cache, pool, q, lens, table, scale=0.25)
+    wide = torch.full((2, 1, 9, D), 7.0, dtype=torch.float16, device="cuda")
+    wide[:, :, :4] = cuda(q)
+    out = torch.full((2, 1, 6, D), 7.0, dtype=torch.float16, device="cuda")
+    zt.KvAttention(cache, wide[:, :, :4], cuda(np.array(lens, np.int32)), cuda(table), scale=0.25, out=out[:, :, 1:5]).run()
+    out = out.cpu().numpy()
+    assert np.array_equal(out[:, :, 1:5], got) and (out[:, :, 0] == 7).all() and (out[:, :, 5] == 7).all()
+
+
+@pytest.mark.parametrize("v_by", [1e-4, 100.0, 8000.0])
+def test_attention_value_ranges(zt, v_by):
+    """Tiny values, and scales of 2 and more, which change the weights' offset within a segment."""
+    rng = np.random.default_rng(6)
+    lens = [200, 33]
+
+    def edit(b, p, k, v):
+        if v_by > 1 and p % 3:
+            v[:] = v / np.float16(v_by)
+    cache, pool, table = filled(zt, rng, lens, 16, 2, 128, v_by=v_by, edit=edit)
+    check_attention(zt, cache, pool, fp16(rng, 2, 1, 4, 128, by=2.0), lens, table, large_v=v_by > 1)
+
+
+def test_attention_sink(zt):
+    """One token takes half the weight, thousands of others share the rest: none of it is lost."""
+    rng = np.random.default_rng(7)
+    D, n = 64, 4000
+    u = np.sign(fp16(rng, D)).astype(np.float16)
+
+    def edit(b, p, k, v):
+        k[:] = u * np.float16(1.0 if p == 0 else 0.0)
+        v[:] = np.float16(0.02) if p else np.float16(0)
+    cache, pool, table = filled(zt, rng, [n], 16, 1, D, edit=edit)
+    q = np.broadcast_to(u, (1, 1, 2, D)).copy()
+    q[0, 0, 1] *= np.float16(2)
+    got = check_attention(zt, cache, pool, q, [n], table, scale=np.log(n) / D)
+    assert (got[0, 0, 0] > 0.009).all() and (got[0, 0, 1] > 0).all()
+
+
+def test_attention_hides_what_is_behind(zt):
+    """NaN scales behind the sequences' ends (random bytes elsewhere in the tests) and NaN rows that an earlier drafted
+    token must not see stay out of the results; rows that see a NaN give NaN."""
+    rng = np.random.default_rng(8)
+    lens, tokens, D = [19, 5], 3, 96
+
+    def edit(b, p, k, v):
+        if p == lens[b] - 1:
+            v[0, 40] = np.nan
+            k[1, 3] = np.inf
+    cache, pool, table = filled(zt, rng, lens, 16, 2, D, edit=edit)
+    got = check_attention(zt, cache, pool, fp16(rng, 2, tokens, 2, D), lens, table)
+    assert np.isfinite(got[:, :2]).all() and np.isnan(got[:, 2, 0, 32:64]).all() and np.isnan(got[:, 2, 1]).all()
+    assert np.isfinite(got[:, 2, 0, :32]).all()
+
+
+def test_attention_reports_bad_pages_and_lengths(zt):
+    """A page out of range is left out with the error bit set; lengths beyond the table are cut, negative ones empty."""
+    import torch
+    rng = np.random.default_rng(9)
+    lens = [40, 33, 16]
+    cache, pool, table = filled(zt, rng, lens, 16, 1, 64)
+    q = fp16(rng, 3, 1, 1, 64)
+    broken = table.copy()
+    broken[0, 1] = pool.raw.shape[0]
+    out = zt.KvAttention(cache, cuda(q), cuda(np.array(lens, np.int32)), cuda(broken)).run().cpu().numpy()
+    assert cache.errors() == zt.ZT_Q4_KV_ERR_PLACE
+    cache.clear_errors()
+    k, v = pool.values(table[0, :3], 40)
+    keep = np.r_[0:16, 32:40]
+    want, mag = ref.attention(q[0], k[keep], v[keep], [24], 64 ** -0.5)
+    assert (np.abs(out[0] - want) <= 2.0**-9 * mag + 2.0**-11 * np.abs(want) + 2.0**-25).all()
+    good = table.copy()
+    good[good > 10**6] = 0
+    out = zt.KvAttention(cache, cuda(q), cuda(np.array([-5, 33, 10**9], np.int32)), cuda(good)).run()
+    torch.cuda.synchronize()
+    assert cache.errors() == zt.ZT_Q4_KV_ERR_PLACE and (out[0] == 0).all() and torch.isfinite(out[1]).all()
+
+
+def test_graph_stream_and_workspace(zt):
+    """Captured and replayed with new contents, and on a stream of its own, the calls give what eager calls give; two graphs
+    that share a workspace may follow each other."""
+    import torch
+    rng = np.random.default_rng(10)
+    lens, heads, D, page = [70, 1500, 3], 2, 128, 16
+    cache, pool, table = filled(zt, rng, lens, page, heads, D)
+    q = cuda(fp16(rng, 3, 1, 4, D))
+    ld, td = cuda(np.array(lens, np.int32)), cuda(table)
+    first = zt.KvAttention(cache, q, ld, td)
+    ws = first._keep[5]
+    second = zt.KvAttention(cache, q.flip(0).contiguous(), ld, td, workspace=ws)
+    want = [first.run().clone(), second.run().clone()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for plan in (first, second):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                plan.run()
+            graphs.append(g)
+        for _ in range(3):
+            for g, plan, w in zip(graphs, (first, second), want):
+                plan._result.zero_()
+                g.replay()
+                assert torch.equal(plan._result, w)
+        q.mul_(0.5)
+        first._result.zero_()
+        graphs[0].replay()
+        replayed = first._result.clone()
+        assert torch.equal(first.run(stream=side), replayed) and not torch.equal(replayed, want[0])
+    torch.cuda.synchronize()
