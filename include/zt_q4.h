@@ -491,6 +491,30 @@ ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, i
                               float scale, uint16_t *out, int ld_out, void *workspace, size_t ws_bytes,
                               void *stream);
 
+/*
+ * Attention over whole prompts (Zero-TVM write-up, limitations section: batched
+ * prefill; the step between the QKV projection and the output projection), fp16
+ * in and out, on the tcgen05 tensor cores.  Sequences are packed: tokens
+ * cu_q[b] .. cu_q[b+1]-1 of q and out [total_q][ld], cu_k[b] .. cu_k[b+1]-1 of k
+ * and v [total_k][ld] (cu_q, cu_k: int32 [n_seqs + 1], DEVICE).  With nq queries
+ * and nk keys in a sequence, query i sees
+ *   all nk keys (causal 0), or the first i + 1 + nk - nq (causal 1: the last
+ *   query sees every key; a chunk behind a prefix has nk > nq),
+ * and out = softmax(scale * q . k) v over them; a query that sees no key gives zeros.
+ * Rows of q, k, v and out hold q_heads or kv_heads heads of head_dim (64, 96 or
+ * 128) side by side, ld elements apart (multiples of 8; 16-byte aligned bases);
+ * q_heads a multiple of kv_heads; n_seqs <= ZT_Q4_KV_MAX_SEQS; total_q, total_k
+ * 0 .. 2^24 (pointers to tensors without rows are not looked at).  Rows of out that no sequence covers are left as they were.
+ * A sequence whose offsets decrease or leave total_q (total_k) is treated as one
+ * without queries (keys).  Scores, softmax statistics and sums are fp32; the
+ * weights are rounded to fp16 for the second product.  err (DEVICE, 4-byte
+ * aligned, or NULL): bit 1 is OR-ed in if a bounded wait (2 s) ran out.  One launch.
+ */
+ZT_API int zt_q4_prompt_attention(const uint16_t *q, int ld_q, const uint16_t *k, int ld_k, const uint16_t *v,
+                                  int ld_v, const int32_t *cu_q, const int32_t *cu_k, int n_seqs, int total_q,
+                                  int total_k, int q_heads, int kv_heads, int head_dim, int causal, float scale,
+                                  uint16_t *out, int ld_out, uint32_t *err, void *stream);
+
 /* Synchronous read of an error word (kv->err or the err of zt_q4_prompt_attention). */
 ZT_API int zt_q4_kv_errors(const uint32_t *err, unsigned int *out);
 
@@ -515,7 +539,8 @@ ZT_API const char *zt_q4_strerror(int status);
 ZT_API const char *zt_q4_last_cuda_error(void);
 
 /* Library ABI version, (major << 16) | minor.  1.3 added zt_q4_pass_plan; 1.4 its column_blocks; 1.5 its
- * warps_per_cta; 1.6 zt_q4_build_flags and zt_q4_pass_test_cut; 1.7 the paged 4-bit KV cache (zt_q4_kv_*). */
+ * warps_per_cta; 1.6 zt_q4_build_flags and zt_q4_pass_test_cut; 1.7 the paged 4-bit KV cache (zt_q4_kv_*)
+ * and zt_q4_prompt_attention. */
 ZT_API int zt_q4_version(void);
 
 #ifdef __cplusplus

@@ -7,7 +7,7 @@ compute name without the library raises ImportError.
 """
 _BINDING = ("gemv", "gate_up_silu", "lmhead_argmax", "lmhead_workspace_bytes",
             "pack_host", "unpack_host", "strerror", "version", "ZtError",
-            "KvCache", "KvAppend", "KvGather", "KvCopy", "KvAttention", "kv_page_bytes")
+            "KvCache", "KvAppend", "KvGather", "KvCopy", "KvAttention", "PromptAttention", "kv_page_bytes")
 
 
 def __getattr__(name):

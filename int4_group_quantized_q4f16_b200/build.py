@@ -23,7 +23,8 @@ LIB_CHECKED = os.path.join(PKG, "libzt_q4_checked.so")
 BUILD = os.path.join(PKG, "build")
 # each source with the headers of csrc/ that it includes
 SOURCES = {"zt_q4.cu": ["zt_host.h", "q4_common.cuh", "q4_mma.cuh", "q4_pass.cuh", "q4_gemm_tc.cuh", "tc_common.cuh"],
-           "zt_kv.cu": ["zt_host.h", "tc_common.cuh", "kv_common.cuh", "kv_cache.cuh", "kv_attn.cuh"],
+           "zt_kv.cu": ["zt_host.h", "tc_common.cuh", "kv_common.cuh", "kv_cache.cuh", "kv_attn.cuh",
+                        "attn_tc.cuh"],
            "zt_host.cu": ["zt_host.h"]}
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]

@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "zt_host.h"
+#include "attn_tc.cuh"
 #include "kv_attn.cuh"
 #include "kv_cache.cuh"
 #include "zt_q4.h"
@@ -143,6 +144,62 @@ template <int D>
 int launch_attention(KvAttnArgs &a, void *stream)
 {
     return column_tiles(a.cols) == 1 ? launch_attention<D, 1>(a, stream) : launch_attention<D, 2>(a, stream);
+}
+
+// fp16 [tokens][heads][D] with rows ld elements apart, boxes of 64 columns x 1 head x 128 tokens, 128-byte
+// swizzle; columns and tokens out of range read as zero.
+bool tma_map_heads(CUtensorMap *map, const uint16_t *base, int D, int heads, int64_t tokens, int ld)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tma_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
+    cuuint32_t box[3] = {64, 1, kAttnRows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_prompt(PromptArgs &a, const uint16_t *q, int ld_q, const uint16_t *k, int ld_k, const uint16_t *v, int ld_v,
+                  void *stream)
+{
+    using C = PromptCfg<D>;
+    int sms = 0;
+    if (resident_ctas(reinterpret_cast<const void *>(&prompt_attn_kernel<D>), kAttnThreads, C::kSmem, sms) < 1)
+        return ZT_ERR_DEVICE;
+    const int kv_heads = a.q_heads / a.group;
+    CUtensorMap mq, mk, mv;
+    if (a.total_k == 0) {             // no keys are read: any valid map will do
+        k = v = q;
+        ld_k = ld_v = ld_q;
+    }
+    const int64_t keys = std::max(a.total_k, 1);
+    if (!tma_map_heads(&mq, q, D, a.q_heads, a.total_q, ld_q) || !tma_map_heads(&mk, k, D, kv_heads, keys, ld_k) ||
+        !tma_map_heads(&mv, v, D, kv_heads, keys, ld_v))
+        return ZT_ERR_DEVICE;
+    // one query tile per CTA while two would leave SMs without work
+    auto items = [&](int tiles) {
+        return ((int64_t)a.total_q + tiles * kAttnRows - 1) / (tiles * kAttnRows) * a.q_heads;
+    };
+    a.tiles = items(2) < sms ? 1 : 2;
+    // every sequence may end with a partial block; CTAs without an item end at once
+    const int64_t grid = items(a.tiles) + (int64_t)(a.n_seqs - 1) * a.q_heads;
+    if (grid > INT_MAX) return ZT_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    clear_stale_error();
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_attn_kernel<D>, mq, mk, mv, (const PromptArgs &)a);
+    return e == cudaSuccess ? ZT_OK : device_error(e, ZT_ERR_LAUNCH);
 }
 
 }  // namespace
@@ -284,6 +341,41 @@ int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, int q_he
     if (kv->head_dim == 64) return launch_attention<64>(a, stream);
     if (kv->head_dim == 96) return launch_attention<96>(a, stream);
     return launch_attention<128>(a, stream);
+}
+
+int zt_q4_prompt_attention(const uint16_t *q, int ld_q, const uint16_t *k, int ld_k, const uint16_t *v, int ld_v,
+                           const int32_t *cu_q, const int32_t *cu_k, int n_seqs, int total_q, int total_k, int q_heads,
+                           int kv_heads, int head_dim, int causal, float scale, uint16_t *out, int ld_out, uint32_t *err,
+                           void *stream)
+{
+    if (!cu_q || !cu_k || n_seqs < 1 || n_seqs > ZT_Q4_KV_MAX_SEQS || total_q < 0 || total_q > kRowsMax || total_k < 0 ||
+        total_k > kRowsMax)
+        return ZT_ERR_INVALID_ARG;
+    if (kv_heads < 1 || kv_heads > 1024 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 16384) return ZT_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128) return ZT_ERR_UNSUPPORTED;
+    if ((causal != 0 && causal != 1) || !(scale > 0.f) || !std::isfinite(scale)) return ZT_ERR_INVALID_ARG;
+    const int64_t qw = (int64_t)q_heads * head_dim, kw = (int64_t)kv_heads * head_dim;
+    int rc;
+    if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(err, 4)) return ZT_ERR_MISALIGNED;
+    if (total_q && ((rc = check_matrix(q, ld_q, qw)) || (rc = check_matrix(out, ld_out, qw)))) return rc;
+    if (total_k && ((rc = check_matrix(k, ld_k, kw)) || (rc = check_matrix(v, ld_v, kw)))) return rc;
+    if (total_q == 0) return ZT_OK;
+    PromptArgs a = {};
+    a.out = h(out);
+    a.ld_out = ld_out;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.n_seqs = n_seqs;
+    a.total_q = total_q;
+    a.total_k = total_k;
+    a.q_heads = q_heads;
+    a.group = q_heads / kv_heads;
+    a.causal = causal;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err = err;
+    if (head_dim == 64) return launch_prompt<64>(a, q, ld_q, k, ld_k, v, ld_v, stream);
+    if (head_dim == 96) return launch_prompt<96>(a, q, ld_q, k, ld_k, v, ld_v, stream);
+    return launch_prompt<128>(a, q, ld_q, k, ld_k, v, ld_v, stream);
 }
 
 int zt_q4_kv_errors(const uint32_t *err, unsigned int *out)

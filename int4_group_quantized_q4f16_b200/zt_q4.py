@@ -143,6 +143,9 @@ def _load() -> ctypes.CDLL:
     lib.zt_q4_kv_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.zt_q4_kv_attention.argtypes = [ctypes.POINTER(ZtKv), _P, _I, _I, _I, _P, _P, _I, _I, ctypes.c_float, _P, _I,
                                        _P, ctypes.c_size_t, _P]
+    lib.zt_q4_prompt_attention.argtypes = [_P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float,
+                                           _P, _I, _P, _P]
+    lib.zt_q4_prompt_attention.restype = ctypes.c_int
     lib.zt_q4_kv_errors.argtypes = [_P, ctypes.POINTER(ctypes.c_uint)]
     for f in (lib.zt_q4_kv_append, lib.zt_q4_kv_gather, lib.zt_q4_kv_copy_pages, lib.zt_q4_kv_attention,
               lib.zt_q4_kv_errors):
@@ -717,3 +720,34 @@ class KvAttention(_Launch):
         row = t.stride(1) if tokens > 1 else t.stride(0)
         flat = t.as_strided((seqs * tokens, t.shape[2], t.shape[3]), (row, t.stride(2), t.stride(3)), t.storage_offset())
         return _heads(flat, dev, what, seqs * tokens, heads, dim)
+
+
+class PromptAttention(_Launch):
+    """Attention over packed prompts: q fp16 [total_q, q_heads, head_dim], k and v fp16 [total_k, kv_heads, head_dim]
+    (rows may be strided: views into a QKV buffer), cu_q and cu_k int32 [n_seqs + 1] offsets of the sequences.  Causal:
+    query i of a sequence with nq queries and nk keys sees the first i + 1 + nk - nq keys; a query that sees none gets
+    zeros.  run() returns out, contiguous when not given.  scale defaults to head_dim ** -0.5.  errors() reads the error
+    word (synchronous; 0 unless a bounded wait ran out)."""
+
+    def __init__(self, q, k, v, cu_q, cu_k, causal: bool = True, out=None, scale=None):
+        torch = _torch()
+        if not q.is_cuda or q.dim() != 3 or k.dim() != 3:
+            raise ValueError("q and k must be 3-D CUDA tensors")
+        dev, (total_q, heads, dim), (total_k, kv_heads) = q.device, (int(n) for n in q.shape), (int(n) for n in k.shape[:2])
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+        (qp, ld_q), (kp, ld_k), (vp, ld_v), (op, ld_o) = (
+            _heads(t, dev, what, n, h, dim) for t, what, n, h in
+            ((q, "q", total_q, heads), (k, "k", total_k, kv_heads), (v, "v", total_k, kv_heads), (out, "out", total_q, heads)))
+        self.err = torch.zeros((1,), dtype=torch.int32, device=dev)
+        seqs = int(cu_q.numel()) - 1
+        super().__init__("zt_q4_prompt_attention", dev,
+                         (qp, ld_q, kp, ld_k, vp, ld_v, _ints(cu_q, dev, "cu_q"), _ints(cu_k, dev, "cu_k", 1, seqs + 1), seqs,
+                          total_q, total_k, heads, kv_heads, dim, int(bool(causal)),
+                          float(dim ** -0.5 if scale is None else scale), op, ld_o, self.err.data_ptr()),
+                         (q, k, v, cu_q, cu_k, out), out)
+
+    def errors(self) -> int:
+        v = ctypes.c_uint(0)
+        _check(lib.zt_q4_kv_errors(self.err.data_ptr(), ctypes.byref(v)), "zt_q4_kv_errors")
+        return int(v.value)

@@ -127,6 +127,25 @@ def test_attention_refusals(zt):
         assert call(**bad) == status(zt, name), bad
 
 
+def test_prompt_refusals(zt):
+    def call(q=FAKE, ld_q=512, k=FAKE, ld_k=128, v=FAKE, ld_v=128, cu_q=FAKE, cu_k=FAKE, seqs=2, total_q=10, total_k=10,
+             heads=8, kv_heads=2, dim=64, causal=1, scale=0.1, out=FAKE, ld=512, err=None):
+        return zt.lib.zt_q4_prompt_attention(q, ld_q, k, ld_k, v, ld_v, cu_q, cu_k, seqs, total_q, total_k, heads, kv_heads,
+                                             dim, causal, scale, out, ld, err, None)
+    for bad, name in ((dict(q=None), "INVALID_ARG"), (dict(k=None), "INVALID_ARG"), (dict(v=None), "INVALID_ARG"),
+                      (dict(out=None), "INVALID_ARG"), (dict(cu_q=None), "INVALID_ARG"), (dict(cu_k=None), "INVALID_ARG"),
+                      (dict(ld_q=504), "INVALID_ARG"), (dict(ld_k=120), "INVALID_ARG"), (dict(ld_v=120), "INVALID_ARG"),
+                      (dict(ld=504), "INVALID_ARG"), (dict(ld_q=516), "MISALIGNED"), (dict(ld_k=132), "MISALIGNED"),
+                      (dict(q=FAKE + 8), "MISALIGNED"), (dict(out=FAKE + 2), "MISALIGNED"), (dict(v=FAKE + 4), "MISALIGNED"),
+                      (dict(cu_q=FAKE + 2), "MISALIGNED"), (dict(err=FAKE + 2), "MISALIGNED"), (dict(seqs=0), "INVALID_ARG"),
+                      (dict(seqs=4097), "INVALID_ARG"), (dict(total_q=-1), "INVALID_ARG"), (dict(total_k=2**25), "INVALID_ARG"),
+                      (dict(heads=7), "INVALID_ARG"), (dict(kv_heads=0), "INVALID_ARG"), (dict(heads=1), "INVALID_ARG"),
+                      (dict(dim=80), "UNSUPPORTED"), (dict(dim=256), "UNSUPPORTED"), (dict(causal=2), "INVALID_ARG"),
+                      (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG")):
+        assert call(**bad) == status(zt, name), bad
+    assert call(total_q=0, q=None, out=None) == zt.ZT_OK
+
+
 def test_errors_call_refusals(zt):
     assert zt.lib.zt_q4_kv_errors(None, ctypes.byref(ctypes.c_uint(0))) == zt.ZT_ERR_INVALID_ARG
     assert zt.lib.zt_q4_kv_errors(FAKE, None) == zt.ZT_ERR_INVALID_ARG

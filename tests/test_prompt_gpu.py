@@ -1,0 +1,193 @@
+"""GPU parity of attention over packed prompts (tcgen05) against float64 (kv_reference.attention).
+
+Tolerances.  A weight is rounded to fp16 (2^-11); scores carry their fp32 accumulation error and that of the exponent's
+argument, together below 2^-16 (|score| log2(e) scale stays below 64: 64 * 2^-24, and D products summed in fp32: D 2^-24
+sum |q k| scale log2(e) < 2^-17), which moves weights by less than 2^-15; weights below 2^-14 of the reference lose up to
+2^-25 of it each, and the reference may lie 2^8 below the largest: 2^-25 max|v| a key.  The output's own rounding adds half
+an fp16 step: in all (2^-11 + 2^-15) sum w |v| + 2^-11 |o| + n 2^-25 max|v| + 2^-25."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def zt():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from int4_group_quantized_q4f16_b200 import zt_q4
+    return zt_q4
+
+
+def cuda(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def fp16(rng, *shape, by=1.0):
+    return (rng.standard_normal(shape) * by).astype(np.float16)
+
+
+def offsets(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+def check(got, q, k, v, nq, nk, causal, scale, heads=None):
+    cq, ck = offsets(nq), offsets(nk)
+    heads = range(q.shape[1]) if heads is None else heads
+    group = q.shape[1] // k.shape[1]
+    for b, (n, m) in enumerate(zip(nq, nk)):
+        for h in heads:
+            qq, g = q[cq[b]:cq[b] + n, [h]], got[cq[b]:cq[b] + n, h]
+            kk, vv = (x[ck[b]:ck[b] + m, [h // group]].astype(np.float64) for x in (k, v))
+            with np.errstate(all="ignore"):
+                want, mag = ref.attention(qq, kk, vv, [i + 1 + m - n if causal else m for i in range(n)], scale)
+            want, mag = want[:, 0], mag[:, 0]
+            top = np.nanmax(np.abs(np.where(np.isfinite(vv), vv, np.nan)), initial=0.0) if m else 0.0
+            tol = (2.0**-11 + 2.0**-15) * mag + 2.0**-11 * np.abs(want) + m * 2.0**-25 * top + 2.0**-25
+            assert np.array_equal(np.isnan(g), np.isnan(want)), (b, h, "NaN in other places")
+            fine = np.isfinite(want)
+            with np.errstate(invalid="ignore"):
+                bad = ((np.abs(g.astype(np.float64) - want) > tol) & fine) | (~fine & ~np.isnan(want) & (g != want))
+            assert not bad.any(), (b, h, np.argwhere(bad)[:4].tolist(), float(np.abs(g.astype(np.float64) - want)[fine].max()))
+
+
+def run(zt, q, k, v, nq, nk, causal=True, scale=None, **more):
+    import torch
+    plan = zt.PromptAttention(cuda(q), cuda(k), cuda(v), cuda(offsets(nq)), cuda(offsets(nk)), causal=causal, scale=scale, **more)
+    got = plan.run().cpu().numpy()
+    again = plan.run().cpu().numpy()
+    torch.cuda.synchronize()
+    assert plan.errors() == 0
+    assert np.array_equal(again.view(np.uint16), got.view(np.uint16)), "two runs differ"
+    return got
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,heads,kv", [(64, 2, 2), (96, 2, 1), (128, 3, 1)])
+@pytest.mark.parametrize("nq,nk", [
+    ([1], [1]), ([45], [45]), ([128], [128]), ([129], [129]), ([300], [300]),
+    ([1, 0, 17, 128, 40, 257], [1, 0, 17, 128, 40, 257]),        # packed, one empty
+    ([5, 130, 64], [200, 131, 64]),                               # chunks behind a prefix
+    ([200, 7, 140], [3, 0, 139]),                                 # fewer keys than queries: rows that see nothing
+])
+def test_prompt(zt, D, heads, kv, nq, nk, causal):
+    rng = np.random.default_rng(D + sum(nq) + sum(nk))
+    q, k, v = fp16(rng, sum(nq), heads, D, by=1.5), fp16(rng, sum(nk), kv, D), fp16(rng, sum(nk), kv, D)
+    check(run(zt, q, k, v, nq, nk, causal), q, k, v, nq, nk, causal, D ** -0.5)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_prompt_many_blocks(zt, D):
+    """Enough heads and rows that a CTA takes two query tiles (checked on a few heads)."""
+    rng = np.random.default_rng(D)
+    nq, nk, heads = [700, 513, 31], [700, 1100, 31], 48
+    q, k, v = fp16(rng, sum(nq), heads, D, by=1.5), fp16(rng, sum(nk), 12, D), fp16(rng, sum(nk), 12, D)
+    check(run(zt, q, k, v, nq, nk), q, k, v, nq, nk, True, D ** -0.5, heads=[0, 7, 47])
+
+
+def test_prompt_long(zt):
+    rng = np.random.default_rng(2)
+    nq, D = [4100], 128
+    q, k, v = fp16(rng, 4100, 1, D, by=2.0), fp16(rng, 4100, 1, D), fp16(rng, 4100, 1, D)
+    check(run(zt, q, k, v, nq, nq), q, k, v, nq, nq, True, D ** -0.5)
+
+
+def test_prompt_strides_scale_and_other_rows(zt):
+    """Views into a QKV buffer, out within a wider one: rows no sequence covers and the heads beside stay as they were."""
+    import torch
+    rng = np.random.default_rng(3)
+    D, heads, kv, n = 96, 4, 2, 150
+    qkv = fp16(rng, n + 20, heads + 2 * kv, D)
+    dev = cuda(qkv)
+    out = torch.full((n + 20, heads + 2, D), 7.0, dtype=torch.float16, device="cuda")
+    cu = cuda(np.array([0, 50, n], np.int32))
+    zt.PromptAttention(dev[:, :heads], dev[:, heads:heads + kv], dev[:, heads + kv:], cu, cu, scale=0.3, out=out[:, 1:-1]).run()
+    out = out.cpu().numpy()
+    q, k, v = qkv[:n, :heads], qkv[:n, heads:heads + kv], qkv[:n, heads + kv:]
+    check(out[:n, 1:-1], q, k, v, [50, 100], [50, 100], True, 0.3)
+    assert (out[n:] == 7).all() and (out[:, 0] == 7).all() and (out[:, -1] == 7).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_ignores_what_is_behind_a_sequence(zt, causal):
+    """NaN and infinities in the next sequence's rows, and in rows that no sequence covers, stay out."""
+    rng = np.random.default_rng(4)
+    D, nq = 128, [37, 5, 129]
+    q, k, v = (fp16(rng, sum(nq) + 60, 2, D) for _ in range(3))
+    for x in (q, k, v):
+        x[37:42] = np.nan
+        x[sum(nq):] = np.inf
+    got = run(zt, q, k, v, nq, nq, causal)
+    assert np.isnan(got[37:42]).all()
+    clean = [0, 1, 2]
+    for b, at in ((0, slice(0, 37)), (2, slice(42, 171))):
+        check(got[at], q[at], k[at], v[at], [nq[b]], [nq[b]], causal, D ** -0.5)
+
+
+def test_prompt_rescales(zt):
+    """Scores that climb by far more than the slack from tile to tile, and fall again; weights that vanish in between."""
+    rng = np.random.default_rng(5)
+    D, n = 64, 600
+    q, k, v = np.ones((n, 1, D), np.float16), np.ones((n, 1, D), np.float16), fp16(rng, n, 1, D)
+    k *= np.array([0, 3, -4, 7, 2], np.float16).repeat(120)[:, None, None]
+    q[::7] *= np.float16(-1)
+    check(run(zt, q, k, v, [n], [n], scale=0.1), q, k, v, [n], [n], True, 0.1)
+
+
+def test_prompt_bad_offsets_are_left_out(zt):
+    """Offsets that decrease or leave the tensors: those sequences count as empty, nothing else is touched."""
+    import torch
+    rng = np.random.default_rng(6)
+    D, n = 64, 100
+    q, k, v = (fp16(rng, n, 1, D) for _ in range(3))
+    out = torch.full((n, 1, D), 7.0, dtype=torch.float16, device="cuda")
+    cu_q = np.array([0, 40, 10, 2**31 - 1, -7, 30], np.int32)     # only [0, 40) is a sequence of q
+    cu_k = np.array([0, 40, 40, 40, 40, 40], np.int32)
+    plan = zt.PromptAttention(cuda(q), cuda(k), cuda(v), cuda(cu_q), cuda(cu_k), out=out)
+    plan.run()
+    got = out.cpu().numpy()
+    assert plan.errors() == 0
+    check(got[:40], q[:40], k[:40], v[:40], [40], [40], True, D ** -0.5)
+    assert (got[40:] == 7).all()
+    cu_k[1] = n + 1                                                 # no keys then: zeros
+    zt.PromptAttention(cuda(q), cuda(k), cuda(v), cuda(cu_q), cuda(cu_k), out=out).run()
+    got = out.cpu().numpy()
+    assert (got[:40] == 0).all() and (got[40:] == 7).all()
+
+
+def test_prompt_without_rows_or_keys(zt):
+    import torch
+    e = lambda n: torch.empty((n, 2, 64), dtype=torch.float16, device="cuda")   # noqa: E731
+    cu = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")            # noqa: E731
+    assert zt.PromptAttention(e(0), e(3), e(3), cu(0, 0), cu(0, 3)).run().shape == (0, 2, 64)
+    out = zt.PromptAttention(torch.ones_like(e(4)), e(0), e(0), cu(0, 4), cu(0, 0), causal=False).run()
+    assert (out == 0).all()
+
+
+def test_prompt_graph_and_stream(zt):
+    import torch
+    rng = np.random.default_rng(7)
+    nq = [300, 20]
+    q, k, v = (cuda(fp16(rng, 320, 2, 96)) for _ in range(3))
+    cu = cuda(offsets(nq))
+    plan = zt.PromptAttention(q, k, v, cu, cu)
+    want = plan.run().clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            plan.run()
+        for _ in range(2):
+            plan._result.zero_()
+            g.replay()
+            assert torch.equal(plan._result, want)
+        v.mul_(2)
+        g.replay()
+        replayed = plan._result.clone()
+        assert torch.equal(plan.run(stream=side), replayed) and not torch.equal(replayed, want)
+    torch.cuda.synchronize()
