@@ -411,7 +411,7 @@ ZT_API int zt_q4_gemm_f16w_gate_up_silu(const uint16_t *w16, const uint16_t *x, 
  */
 #define ZT_Q4_KV_ERR_PLACE 1u
 #define ZT_Q4_KV_ERR_WAIT 2u
-#define ZT_Q4_KV_MAX_SEQS 4096
+#define ZT_Q4_KV_MAX_SEQS 2048
 
 typedef struct zt_q4_kv {
     void *pages;              /* DEVICE, 16-byte aligned: n_pages pages of zt_q4_kv_page_bytes() bytes */
@@ -483,7 +483,7 @@ ZT_API int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int
  * before and after they are multiplied by V's scales.
  * workspace: DEVICE, 16-byte aligned, zt_q4_kv_attention_workspace_bytes() bytes
  * (a function of these sizes alone); contents on entry do not matter.  Calls that
- * may overlap need workspaces of their own.  Two launches.
+ * may overlap need workspaces of their own.  One or two launches.
  */
 ZT_API size_t zt_q4_kv_attention_workspace_bytes(int kv_heads, int q_heads, int head_dim, int tokens);
 ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, int q_heads, int tokens,

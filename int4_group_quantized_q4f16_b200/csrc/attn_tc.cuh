@@ -31,7 +31,6 @@ namespace zt {
 
 constexpr int kAttnRows = 128, kAttnKeys = 128;
 constexpr int kAttnThreads = 384;
-constexpr int kAttnSeqs = 4096;
 constexpr float kAttnSlack = 8.f;      // log2 of the largest weight before a rescale
 
 struct PromptArgs {

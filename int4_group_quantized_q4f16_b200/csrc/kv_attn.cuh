@@ -3,7 +3,7 @@
 //
 // Mathematics.  For a kv head, the columns are its (query token, query head)
 // pairs; per tile of 16 cached tokens
-//   S[t][c] = sum_g ks[t][g] (sum_{d in g} kc[t][d] q[d][c] - 7 sum_{d in g} q[d][c])
+//   S[t][c] = sum_g ks[t][g] sum_{d in g} kc[t][d] q[d][c]  +  sum_g ks[t][g] x[g][c],   x[g][c] = -7 sum_{d in g} q[d][c]
 //   p[t][c] = 2^(scale log2(e) S[t][c] - R[c])
 //   O[d][c] += sum_t (vc[t][d] - 7) (p[t][c] vs[t][g(d)])
 // and the result is O[d][c] / sum_t p[t][c].  kc and vc are the 4-bit codes, ks
@@ -29,12 +29,15 @@
 // with a larger scale sets the offset to 0 (p <= 4, p * vs <= 4 * 65504 / 7).
 // p is rounded to fp16, p * vs once more; sums of p and O are fp32.
 //
-// Work split.  The (sequence, kv head) segments are laid end to end in tiles and
-// cut into equal runs, one per CTA, then one per warp: ragged batches and single
-// long sequences balance alike.  Each warp streams its run through a private ring
-// of bulk copies (one copy = one tile, K and V).  Segments cut between warps are
-// joined in shared memory, segments cut between CTAs by kv_attn_join_kernel,
-// always in the order of the tokens: results do not depend on timing.
+// Work split.  The (sequence, kv head) segments are laid end to end in tiles, each
+// with two more that stand for its own cost, and cut into equal runs, one per CTA,
+// then one per warp: ragged batches and single long sequences balance alike.  Each
+// warp streams its run through a private ring of bulk copies (a tile is K and V),
+// two tiles at a time.  Where every segment is short and there are few of them, a
+// CTA takes one whole segment and the second launch is saved.  Segments cut between
+// warps are joined in shared memory, segments cut between CTAs by
+// kv_attn_join_kernel, always in the order of the tokens: results do not depend on
+// timing.
 #pragma once
 
 #include "kv_common.cuh"
@@ -52,6 +55,7 @@ struct KvAttnArgs {
     int q_heads, group;        // group = q_heads / kv_heads
     int cols, blocks;          // columns of a kv head (tokens * group), and blocks of 8 NT of them
     int ctas;                  // CTAs of the main kernel
+    int whole;                 // 1: a CTA takes one whole segment, nothing is left to join
     float scale_log2;          // softmax scale * log2(e)
 };
 
@@ -59,27 +63,33 @@ template <int D, int NT>
 struct KvAttnCfg {
     using T = KvTile<D>;
     static constexpr int kWarps = NT == 1 ? 16 : 8;
-    static constexpr int kStages = 4;
+    static constexpr int kPairs = D == 64 ? 4 : 2;      // ring stages of two tiles
+    static constexpr int kStage = 2 * T::kBytes;
     static constexpr int kCols = 8 * NT;
     static constexpr int kPart = kCols * (D + 2);                      // floats: O, then R and the sum of p per column
-    static constexpr int kRing = kStages * T::kBytes;                  // per warp; holds the last partial at the end
-    static constexpr int kPartBytes = (kPart * 4 + 15) / 16 * 16;
+    static constexpr int kRing = kPairs * kStage;                      // per warp; holds the last partial at the end
+    static constexpr int kPartBytes = (kPart * 4 + 8 + 15) / 16 * 16;         // and the segment, within a CTA
     static_assert(kPartBytes <= kRing, "a warp's last partial goes to its ring");
-    static constexpr int kBars = kWarps * kStages * 8;
-    static constexpr int kFlags = 3 * kWarps * 4;
-    static constexpr int kSmem = kWarps * (kRing + kPartBytes) + kBars + kFlags;   // + the prefix sums, 4 bytes per sequence
+    static constexpr int kBars = kWarps * kPairs * 8;
+    static constexpr int kFlags = kWarps * 4;
+    static constexpr int kSmem = kWarps * (kRing + kPartBytes) + kBars + kFlags;   // + KvIndex, 8 bytes per sequence
 };
 
-constexpr int kKvSeqs = 4096;          // sequences per call (prefix sums in shared memory)
+constexpr int kKvSegTiles = 2;         // what starting and ending a segment costs, in tiles
 constexpr int kKvWarpTiles = 1;        // tiles per warp below which fewer CTAs are used
+constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
 constexpr float kKvOff = 12.f, kKvSlack = 2.f;
 
-// Runs of tiles: CTA c of n takes [T c / n, T (c + 1) / n).
-__device__ __forceinline__ int kv_run(int total, int c, int n) { return (int)((long long)total * c / n); }
-__device__ __forceinline__ int kv_owner(int total, int x, int n)
-{
-    return (int)((((long long)x + 1) * n - 1) / total);
-}
+// Runs of tiles: CTA c of n takes total / n of them, the first total % n CTAs one more.
+struct KvRuns {
+    int each, more;
+    __device__ __forceinline__ KvRuns(int total, int n) : each(total / n), more(total - total / n * n) {}
+    __device__ __forceinline__ int start(int c) const { return each * c + min(c, more); }
+    __device__ __forceinline__ int owner(int x) const
+    {
+        return x < more * (each + 1) ? x / (each + 1) : more + (x - more * (each + 1)) / each;
+    }
+};
 
 // Number of CTAs that share `total` tiles.
 __device__ __forceinline__ int kv_ctas(int total, int ctas, int warps)
@@ -113,10 +123,12 @@ __device__ __forceinline__ uint32_t kv_transpose(uint32_t v)
     return r;
 }
 
-// (code - 7) * 2^-10 of a pair of codes masked out of its word: f undoes the subnormals' 2^-24 (and a high nibble's 16).
-__device__ __forceinline__ uint32_t kv_value(uint32_t codes, float f)
+// (code - 7) * 2^-10 of a pair of codes masked out of its word: the factor (2^14, or 2^10 for the high nibbles' 16
+// times larger patterns) undoes the subnormals' 2^-24.
+constexpr uint32_t kKvLow = 0x74007400u, kKvHigh = 0x64006400u, kKvMinus7 = 0x9F009F00u;
+__device__ __forceinline__ uint32_t kv_value(uint32_t codes, uint32_t f)
 {
-    return h2_bits(__hfma2(bits_h2(codes), __float2half2_rn(f), __float2half2_rn(-7.f * 0x1p-10f)));
+    return h2_bits(__hfma2(bits_h2(codes), bits_h2(f), bits_h2(kKvMinus7)));
 }
 
 __device__ __forceinline__ float kv_exp2(float x)
@@ -139,70 +151,99 @@ __device__ __forceinline__ void kv_lds(uint32_t (&w)[N], uint32_t addr)
         for (int i = 0; i < N; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i));
 }
 
-// prefix[b] = tiles of the sequences before b, each counted for every kv head and column block.
-__device__ __forceinline__ void kv_prefix(const KvAttnArgs &a, int *prefix)
-{
-    const int per = a.at.kv_heads * a.blocks;
-    for (int b = threadIdx.x; b < a.at.n_seqs; b += blockDim.x)
-        prefix[b + 1] = (kv_len(a, b) + kKvTile - 1) / kKvTile * per;
-    if (threadIdx.x == 0) prefix[0] = 0;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        int base = 0;
-        for (int b0 = 0; b0 < a.at.n_seqs; b0 += 32) {
-            const int b = b0 + threadIdx.x;
-            int v = b < a.at.n_seqs ? prefix[b + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if ((int)threadIdx.x >= o) v += u;
-            }
-            if (b < a.at.n_seqs) prefix[b + 1] = base + v;
-            base += __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
-    __syncthreads();
-}
+// The sequences in shared memory: lengths, and first[b] = virtual tiles (with every segment's kKvSegTiles) of the
+// sequences before b.
+struct KvIndex {
+    int *first, *lens;
+    int per, n;                // segments per sequence (kv heads x column blocks), sequences
 
-// A position in the run of tiles: sequence, head-and-block, tile.
+    __device__ __forceinline__ void build(const KvAttnArgs &a, int *mem)
+    {
+        n = a.at.n_seqs;
+        per = a.at.kv_heads * a.blocks;
+        first = mem;
+        lens = mem + n + 1;
+        const int lane = threadIdx.x & 31;
+        if (n <= 32) {
+            // every warp by itself (all write the same)
+            const int len = lane < n ? kv_len(a, lane) : 0;
+            const int upto = scan(lane < n ? ((len + kKvTile - 1) / kKvTile + kKvSegTiles) * per : 0);
+            if (lane < n) {
+                lens[lane] = len;
+                first[lane + 1] = upto;
+            }
+            if (lane == 0) first[0] = 0;
+            __syncwarp();
+            return;
+        }
+        for (int b = threadIdx.x; b < n; b += blockDim.x) lens[b] = kv_len(a, b);
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            int base = 0;
+            for (int b0 = 0; b0 < n; b0 += 32) {
+                const int b = b0 + lane;
+                const int upto = base + scan(b < n ? ((lens[b] + kKvTile - 1) / kKvTile + kKvSegTiles) * per : 0);
+                if (b < n) first[b + 1] = upto;
+                base = __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (lane == 0) first[0] = 0;
+        }
+        __syncthreads();
+    }
+    __device__ static __forceinline__ int scan(int v)
+    {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if ((int)(threadIdx.x & 31) >= o) v += u;
+        }
+        return v;
+    }
+    __device__ __forceinline__ int total() const { return first[n]; }
+};
+
+// A tile: sequence, head-and-block, index within the segment (which may lie behind its last tile, in the virtual ones).
 struct KvCursor {
     int b, hc, tile, tiles, len;
-    __device__ __forceinline__ void seek(const KvAttnArgs &a, const int *prefix, int x)
+    __device__ __forceinline__ void enter(const KvIndex &ix)
     {
-        int lo = 0, hi = a.at.n_seqs;                       // prefix[lo] <= x < prefix[hi]
+        len = ix.lens[b];
+        tiles = (len + kKvTile - 1) / kKvTile;
+    }
+    __device__ __forceinline__ void seek(const KvIndex &ix, int x)
+    {
+        int lo = 0, hi = ix.n;                              // first[lo] <= x < first[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= x) lo = mid;
+            if (ix.first[mid] <= x) lo = mid;
             else hi = mid;
         }
         b = lo;
-        enter(a);
-        const int rel = x - prefix[b];
-        hc = rel / tiles;
-        tile = rel - hc * tiles;
+        enter(ix);
+        const int rel = x - ix.first[b];
+        hc = rel / (tiles + kKvSegTiles);
+        tile = rel - hc * (tiles + kKvSegTiles);
     }
-    __device__ __forceinline__ void enter(const KvAttnArgs &a)
+    // tiles (not virtual ones) before this position, which is x
+    __device__ __forceinline__ int before(const KvIndex &ix, int x) const
     {
-        len = min(max(a.lens[b], 0), a.at.max_pages * a.at.page_size);
-        tiles = (len + kKvTile - 1) / kKvTile;
+        return x - kKvSegTiles * (b * ix.per + hc) - max(0, tile - tiles);
     }
-    // on to the next tile; there is one (the caller counts the run)
-    __device__ __forceinline__ void next(const KvAttnArgs &a)
+    // on to the start of the next segment that has tiles; there is one
+    __device__ __forceinline__ void next_segment(const KvIndex &ix)
     {
-        if (++tile < tiles) return;
         tile = 0;
-        if (++hc < a.at.kv_heads * a.blocks) return;
+        if (++hc < ix.per) return;
         hc = 0;
         do {
-            if (++b >= a.at.n_seqs) {
-                b = 0;                                      // behind the last tile: never used
-                tiles = 1;
-                return;
-            }
-            enter(a);
+            ++b;
+            enter(ix);
         } while (tiles == 0);
     }
 };
+
+// b's halves, zero where p's are.  Kept out of line: it is hardly ever needed.
+static __device__ __noinline__ uint32_t kv_hide(uint32_t b, uint32_t p) { return b & ~__vcmpeq2(p, 0u); }
 
 // Columns of head-and-block hc.
 __device__ __forceinline__ int kv_columns(const KvAttnArgs &a, int hc, int kcols)
@@ -218,104 +259,211 @@ __device__ __forceinline__ __half *kv_out_row(const KvAttnArgs &a, int b, int hc
     return a.out + ((long long)b * a.tokens + i) * a.ld_out + head * D;
 }
 
+// Zeros for the queries of a sequence without tokens: whole CTA.
+__device__ __forceinline__ void kv_zero(const KvAttnArgs &a, int b, int hc, int kcols, int D)
+{
+    for (int i = threadIdx.x; i < kv_columns(a, hc, kcols) * D; i += blockDim.x)
+        kv_out_row(a, b, hc, i / D, kcols, D)[i % D] = __float2half_rn(0.f);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnArgs a)
 {
     using C = KvAttnCfg<D, NT>;
     using T = KvTile<D>;
-    constexpr int G = T::kG, W = C::kWarps, S = C::kStages;
+    constexpr int G = T::kG, W = C::kWarps, S = C::kPairs;
     extern __shared__ __align__(128) unsigned char kv_smem_raw[];
     unsigned char *rings = kv_smem_raw;
     float *heads = reinterpret_cast<float *>(kv_smem_raw + W * C::kRing);      // a warp's first partial
     const uint32_t bars = kv_smem(kv_smem_raw) + W * (C::kRing + C::kPartBytes);
-    int *prefix = reinterpret_cast<int *>(kv_smem_raw + C::kSmem);
+    int *index = reinterpret_cast<int *>(kv_smem_raw + C::kSmem);
     // all shared memory is dynamic: the opt-in limit leaves no room for a static part
-    int *open = prefix - 3 * W;      // 1: the warp's last segment goes on in the next warp
-    int *began = prefix - 2 * W;     // 1: that segment began in this warp
-    int *first = prefix - W;         // 1: the warp wrote a partial of a segment that began earlier and ended in it
+    int *flags = index - W;          // of each warp: 1 it had tiles, 2 its last segment goes on in the next warp,
+                                     // 4 and began in it, 8 it wrote the end of a segment that began earlier
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
-    if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * (warp * S + lane)) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    kv_pdl_launch();
-    kv_pdl_wait();
-    kv_prefix(a, prefix);
-    const int total = prefix[a.at.n_seqs];
-    const int n_ctas = kv_ctas(total, gridDim.x, W);
-    if ((int)blockIdx.x >= n_ctas || total == 0) return;
-    const int c_lo = kv_run(total, blockIdx.x, n_ctas), c_hi = kv_run(total, blockIdx.x + 1, n_ctas);
-    const int lo = c_lo + kv_run(c_hi - c_lo, warp, W), hi = c_lo + kv_run(c_hi - c_lo, warp + 1, W);
-    const int n = hi - lo;
-
     const uint32_t ring = kv_smem(rings) + warp * C::kRing, bar = bars + 8 * warp * S;
+    if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8 * lane) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    kv_pdl_wait();
+    kv_pdl_launch();                 // now the joining kernel may read the lengths too while this one runs
+
+    // this CTA's run of tiles: its share of all of them, or one whole segment
+    KvIndex ix;
+    KvCursor at = {}, seg = {};
+    int c_lo = 0, c_n;
+    if (a.whole) {
+        const int per = a.at.kv_heads * a.blocks;
+        at.b = blockIdx.x / per;
+        at.hc = blockIdx.x - at.b * per;
+        at.len = kv_len(a, at.b);
+        at.tiles = c_n = (at.len + kKvTile - 1) / kKvTile;
+        __syncwarp();
+        if (c_n == 0) {
+            kv_zero(a, at.b, at.hc, C::kCols, D);
+            return;
+        }
+    } else {
+        ix.build(a, index);
+        for (int b = blockIdx.x; b < ix.n; b += gridDim.x)
+            if (ix.lens[b] == 0)
+                for (int hc = 0; hc < ix.per; ++hc) kv_zero(a, b, hc, C::kCols, D);
+        const int total = ix.total(), n_ctas = kv_ctas(total, gridDim.x, W);
+        if ((int)blockIdx.x >= n_ctas) return;
+        const KvRuns runs(total, n_ctas);
+        c_lo = runs.start(blockIdx.x);
+        c_n = runs.start(blockIdx.x + 1) - c_lo;
+    }
+    // this warp's run within it: n tiles from seg on
+    int lo = (int)((long long)c_n * warp / W), hi = (int)((long long)c_n * (warp + 1) / W), n = hi - lo;
+    if (a.whole) {
+        seg = at;
+        seg.tile = lo;
+    } else {
+        lo += c_lo;
+        hi += c_lo;
+        int upto = ix.total() - kKvSegTiles * ix.n * ix.per;
+        if (hi < ix.total()) {
+            seg.seek(ix, hi);
+            upto = seg.before(ix, hi);
+        }
+        seg.seek(ix, lo);
+        n = upto - seg.before(ix, lo);
+        if (n > 0 && seg.tile >= seg.tiles) seg.next_segment(ix);
+    }
+
     float *tail = reinterpret_cast<float *>(rings + warp * C::kRing);
     float *head_part = heads + warp * (C::kPartBytes / 4);
     const int tpp = a.at.page_size / kKvTile;
 
-    // the copying side runs S tiles ahead
+    // The copying side runs kPairs steps ahead.  A step is two tiles of a segment, or one where the segment or
+    // the run ends; src walks through the page that ahead's next tile is in.
     KvCursor ahead = {};
-    unsigned bad = 0;                // stages whose tile has no page
-    auto issue = [&](int s) {
-        const int in_seq = ahead.tile / tpp;
-        const int page = __ldg(a.at.table + (long long)ahead.b * a.at.max_pages + in_seq);
-        bad &= ~(1u << s);
-        if (page < 0 || page >= a.at.n_pages) {
-            bad |= 1u << s;
-            if (lane == 0) {
-                kv_error(a.at.err, kErrKvPlace);
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + 8 * s) : "memory");
-            }
-        } else if (lane == 0) {
-            const int h = ahead.hc / a.blocks;
-            const unsigned char *src = a.at.pages + page * a.at.page_bytes +
-                                       ((long long)h * tpp + (ahead.tile - in_seq * tpp)) * T::kBytes;
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar + 8 * s), "r"(T::kBytes) : "memory");
+    const unsigned char *src = nullptr;
+    int in_page = 0, page_at = 0, to_copy = n;
+    int entry = 0, entry_b = -1, entry_at = 0;      // lane i holds the table's entry entry_at + i of sequence entry_b
+    unsigned bad = 0;                // two bits per stage: tiles that have no page
+    auto open_page = [&]() {
+        if (ahead.b != entry_b || page_at < entry_at || page_at >= entry_at + 32) {
+            entry_b = ahead.b;
+            entry_at = page_at;
+            const int last = (ahead.tiles - 1) / tpp;
+            entry = page_at + lane <= last ? __ldg(a.at.table + (long long)entry_b * a.at.max_pages + page_at + lane) : -1;
+        }
+        const int page = __shfl_sync(0xffffffffu, entry, page_at - entry_at);
+        const bool fine = page >= 0 && page < a.at.n_pages;
+        src = fine ? a.at.pages + page * a.at.page_bytes + ((long long)(ahead.hc / a.blocks) * tpp + in_page) * T::kBytes
+                   : nullptr;
+        if (!fine && lane == 0) kv_error(a.at.err, kErrKvPlace);
+    };
+    auto copy = [&](int s, int u, int tiles) {      // `tiles` tiles from src on, to place u of stage s
+        if (lane == 0 && src)
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                    ring + s * T::kBytes),
-                "l"(src), "r"(T::kBytes), "r"(bar + 8 * s) : "memory");
+                    ring + s * C::kStage + u * T::kBytes),
+                "l"(src), "r"(tiles * T::kBytes), "r"(bar + 8 * s) : "memory");
+    };
+    auto expect = [&](int s, int tiles) {           // a stage's arrival: the bytes of this many tiles
+        if (lane == 0) {
+            if (tiles)
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar + 8 * s), "r"(tiles * T::kBytes)
+                             : "memory");
+            else
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + 8 * s) : "memory");
         }
-        ahead.next(a);
+    };
+    auto next_page = [&]() {
+        in_page = 0;
+        ++page_at;
+        open_page();
+    };
+    auto issue = [&](int s) {
+        const int step = min(min(2, to_copy), ahead.tiles - ahead.tile);
+        if (src && in_page + step <= tpp) {         // both tiles lie side by side
+            expect(s, step);
+            copy(s, 0, step);
+            src += step * T::kBytes;
+            in_page += step;
+            bad &= ~(3u << (2 * s));
+        } else {
+            // from one page to the next, or a page out of range; the next page's address is known before
+            // the stage's bytes are announced
+            const unsigned char *one = src;
+            const unsigned miss0 = src ? 0u : 1u;
+            if (step == 2) {
+                if (++in_page == tpp) next_page();
+                else if (src) src += T::kBytes;
+            }
+            const unsigned miss1 = step == 2 && !src ? 2u : 0u;
+            bad = (bad & ~(3u << (2 * s))) | ((miss0 | miss1) << (2 * s));
+            expect(s, step - (int)miss0 - (int)(miss1 >> 1));
+            const unsigned char *two = src;
+            src = one;
+            copy(s, 0, 1);
+            if (step == 2) {
+                src = two;
+                copy(s, 1, 1);
+            }
+            if (src) src += T::kBytes;
+            ++in_page;
+        }
+        to_copy -= step;
+        if (to_copy == 0) return;
+        ahead.tile += step;
+        if (ahead.tile == ahead.tiles) {
+            ahead.next_segment(ix);
+            in_page = page_at = 0;
+            open_page();
+        } else if (in_page == tpp) {
+            next_page();
+        }
     };
 
-    KvCursor at = {};
     bool is_open = false, did_begin = false, did_first = false;
     if (n > 0) {
-        at.seek(a, prefix, lo);
-        ahead = at;
-        for (int s = 0; s < min(S, n); ++s) issue(s);
+        ahead = seg;
+        page_at = ahead.tile / tpp;
+        in_page = ahead.tile - page_at * tpp;
+        open_page();
+        for (int s = 0; s < C::kPairs && to_copy > 0; ++s) issue(s);
     }
 
-    float O[NT][D / 16][4], R[NT][2], L[NT][2], xg[NT][G][2];
-    uint32_t qf[NT][G][4];
+    float O[NT][D / 16][4], R[NT][2], L[NT][2], most[NT][2];
+    uint32_t qf[NT][G][4], xq[NT];
     int seen[NT][2];                 // tokens that columns 2j and 2j + 1 see
     float off = kKvOff;
+    const float sl = a.scale_log2 * 0x1p24f, inv_sl = 1.f / sl;
     bool fresh = true, dead = false;
-    int seg_tile0 = 0;
-    for (int x = 0; x < n; ++x) {
+    int seg_tile0 = 0, step = 1, s = 0;
+    uint32_t parity = 0;
+    for (int x = 0; x < n; x += step) {
         if (fresh) {
-            // a new segment: its queries as B fragments, the sums of q per group, the columns' ends
+            // a new segment: its queries as B fragments, the zero point's term, the columns' ends
             fresh = false;
-            seg_tile0 = at.tile;
+            seg_tile0 = seg.tile;
             off = kKvOff;
-            const int h = at.hc / a.blocks, c0 = (at.hc - h * a.blocks) * C::kCols;
+            const int h = seg.hc / a.blocks, c0 = (seg.hc - h * a.blocks) * C::kCols;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int col = c0 + nt * 8 + r;
                 const bool has = col < a.cols;
                 const int i = has ? col / a.group : 0, qh = h * a.group + (has ? col - i * a.group : 0);
-                const __half *src = a.q + ((long long)at.b * a.tokens + i) * a.ld_q + qh * D + 8 * j;
+                const __half *q = a.q + ((long long)seg.b * a.tokens + i) * a.ld_q + qh * D + 8 * j;
+                __half xlo = __float2half_rn(0.f), xhi = xlo;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    uint4 w = has ? *reinterpret_cast<const uint4 *>(src + 32 * g) : make_uint4(0, 0, 0, 0);
+                    const uint4 w = has ? *reinterpret_cast<const uint4 *>(q + 32 * g) : make_uint4(0, 0, 0, 0);
                     const float2 f0 = __half22float2(bits_h2(w.x)), f1 = __half22float2(bits_h2(w.y)),
                                  f2 = __half22float2(bits_h2(w.z)), f3 = __half22float2(bits_h2(w.w));
                     float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    // codes are code * 2^-24, so the zero point's term carries the same factor
-                    xg[nt][g][0] = -7.f * 0x1p-24f * __shfl_sync(0xffffffffu, sum, 8 * j);
-                    xg[nt][g][1] = -7.f * 0x1p-24f * __shfl_sync(0xffffffffu, sum, 8 * j + 4);
+                    // lane j of a quad keeps the two groups of its k slots: groups 0..3 rounded to fp16 in
+                    // slots 0..3, what the rounding left in slots 4..7 (2^-8 of them, so that none overflows)
+                    sum *= -7.f * 0x1p-8f;
+                    const __half high = __float2half_rn(sum);
+                    const __half part = j < 2 ? high : __float2half_rn(sum - __half2float(high));
+                    if (g / 2 == (j & 1)) (g & 1 ? xhi : xlo) = part;
                     // step 0 of a group meets codes 0, 4 | 2, 6 of the lane's word, step 1 codes 1, 5 | 3, 7,
                     // which come with a factor 16
                     const __half2 six = __float2half2_rn(0.0625f);
@@ -324,162 +472,202 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                     qf[nt][g][2] = h2_bits(__hmul2(bits_h2(__byte_perm(w.x, w.z, 0x7632)), six));
                     qf[nt][g][3] = h2_bits(__hmul2(bits_h2(__byte_perm(w.y, w.w, 0x7632)), six));
                 }
+                xq[nt] = h2_bits(__halves2half2(xlo, xhi));
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) O[nt][m][e] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    R[nt][e] = -INFINITY;
+                    R[nt][e] = most[nt][e] = -INFINITY;
                     L[nt][e] = 0.f;
-                    seen[nt][e] = at.len - a.tokens + 1 + (c0 + nt * 8 + 2 * j + e) / a.group;
+                    seen[nt][e] = seg.len - a.tokens + 1 + (c0 + nt * 8 + 2 * j + e) / a.group;
                 }
             }
         }
-        const int s = x % S;
-        if (!dead && !__all_sync(0xffffffffu, tc_wait(bar + 8 * s, (uint32_t)(x / S) & 1u, false))) {
-            // the copy did not land in time: report it, give the other copies in flight their time,
-            // and go on without reading tiles (the results are incomplete)
+        // Two tiles at a time, for independent work between the waits and one look at the maxima; a last
+        // odd one goes alone, its missing partner masked.
+        step = min(min(2, n - x), seg.tiles - seg.tile);
+        if (!dead && !__all_sync(0xffffffffu, tc_wait(bar + 8 * s, parity, false))) {
+            // a copy did not land in time: report it, give the other copies in flight their time, and go on
+            // without reading tiles (the results are incomplete)
             if (lane == 0) kv_error(a.at.err, kErrKvWait);
-            for (int y = x + 1; y < min(x + S, n); ++y) tc_wait(bar + 8 * (y % S), (uint32_t)(y / S) & 1u, false);
+            for (int i = 0; i < S && n - x - to_copy > i; ++i)
+                tc_wait(bar + 8 * ((s + i) % S), parity ^ (s + i >= S ? 1u : 0u), false);
             __syncwarp();
             dead = true;
         }
-        if (!dead && !((bad >> s) & 1u)) {
-            const uint32_t tile = ring + s * T::kBytes;
-            float P[NT][4];
-            {
-                uint32_t wa[G], wb[G], ks[G];
-                kv_lds<G>(wa, tile + (r * 4 + j) * G * 4);
-                kv_lds<G>(wb, tile + ((r + 8) * 4 + j) * G * 4);
-                kv_lds<G>(ks, tile + T::kKs + r * G * 4);
+        const bool drop0 = dead || ((bad >> (2 * s)) & 1u), drop1 = dead || step < 2 || ((bad >> (2 * s)) & 2u);
+        const uint32_t stage = ring + s * C::kStage;
+        const uint32_t tile[2] = {stage, stage + T::kBytes};
+        float P[NT][2][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) P[nt][e] = 0.f;
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const float2 sc = __half22float2(bits_h2(ks[g]));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float d[4];
-                        kv_mma(d, wa[g] & 0x000F000Fu, wb[g] & 0x000F000Fu, (wa[g] >> 8) & 0x000F000Fu,
-                               (wb[g] >> 8) & 0x000F000Fu, qf[nt][g][0], qf[nt][g][1], xg[nt][g][0], xg[nt][g][1],
-                               xg[nt][g][0], xg[nt][g][1]);
-                        kv_mma(d, wa[g] & 0x00F000F0u, wb[g] & 0x00F000F0u, (wa[g] >> 8) & 0x00F000F0u,
-                               (wb[g] >> 8) & 0x00F000F0u, qf[nt][g][2], qf[nt][g][3], d[0], d[1], d[2], d[3]);
-                        P[nt][0] = fmaf(sc.x, d[0], P[nt][0]);
-                        P[nt][1] = fmaf(sc.x, d[1], P[nt][1]);
-                        P[nt][2] = fmaf(sc.y, d[2], P[nt][2]);
-                        P[nt][3] = fmaf(sc.y, d[3], P[nt][3]);
-                    }
-                }
+        for (int u = 0; u < 2; ++u) {
+            uint32_t wa[G], wb[G], ks[G], kz[2];
+            kv_lds<G>(wa, tile[u] + (r * 4 + j) * G * 4);
+            kv_lds<G>(wb, tile[u] + ((r + 8) * 4 + j) * G * 4);
+            kv_lds<G>(ks, tile[u] + T::kKs + r * G * 4);
+            // this lane's two groups of scales again, by token: the A operand of the zero point's product.  A slot
+            // without a group meets zeros in B; its scale must be this token's, or zero, not another's NaN.
+            if constexpr (G == 4) {
+                kv_lds<2>(kz, tile[u] + T::kKs + (r * G + 2 * (j & 1)) * 4);
+            } else {
+                kz[0] = G == 3 && (j & 1) ? ks[G - 1] : ks[0];
+                kz[1] = G == 3 && (j & 1) ? 0u : ks[1];
             }
-            // the V scales of this lane's tokens 2j, 2j + 1 and 2j + 8, 2j + 9
-            uint32_t vs[2 * G];
+            const uint32_t za = __byte_perm(kz[0], kz[1], 0x5410), zb = __byte_perm(kz[0], kz[1], 0x7632);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                uint32_t w[2];
-                kv_lds<2>(w, tile + T::kVs + (j * G + g) * 8);
-                vs[2 * g] = w[0];
-                vs[2 * g + 1] = w[1];
+                const float2 sc = __half22float2(bits_h2(ks[g]));
+                const uint32_t ha = wa[g] >> 8, hb = wb[g] >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float d[4];
+                    float (&p)[4] = P[nt][u];
+                    kv_mma(d, wa[g] & 0x000F000Fu, wb[g] & 0x000F000Fu, ha & 0x000F000Fu, hb & 0x000F000Fu, qf[nt][g][0],
+                           qf[nt][g][1], 0.f, 0.f, 0.f, 0.f);
+                    kv_mma(d, wa[g] & 0x00F000F0u, wb[g] & 0x00F000F0u, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[nt][g][2],
+                           qf[nt][g][3], d[0], d[1], d[2], d[3]);
+                    p[0] = g ? fmaf(sc.x, d[0], p[0]) : sc.x * d[0];
+                    p[1] = g ? fmaf(sc.x, d[1], p[1]) : sc.x * d[1];
+                    p[2] = g ? fmaf(sc.y, d[2], p[2]) : sc.y * d[2];
+                    p[3] = g ? fmaf(sc.y, d[3], p[3]) : sc.y * d[3];
+                }
             }
-            const int t0 = at.tile * kKvTile;
-            const bool edge = t0 + kKvTile > at.len - a.tokens + 1;      // some column does not see the whole tile
-            if (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float z[4];
+                kv_mma(z, za, zb, 0u, 0u, xq[nt], 0u, 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) P[nt][u][e] = fmaf(z[e], 0x1p-16f, P[nt][u][e]);
+            }
+        }
+        // the V scales of this lane's tokens 2j, 2j + 1 and 2j + 8, 2j + 9
+        uint32_t vs[2][2 * G];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int g = 0; g < G; g += G % 2 ? 1 : 2) {
+                uint32_t w[G % 2 ? 2 : 4];
+                kv_lds<G % 2 ? 2 : 4>(w, tile[u] + T::kVs + (j * G + g) * 8);
+#pragma unroll
+                for (int i = 0; i < (G % 2 ? 2 : 4); ++i) vs[u][2 * g + i] = w[i];
+            }
+        const int t0 = seg.tile * kKvTile;
+        // some column does not see all of both tiles
+        const bool edge = t0 + 2 * kKvTile > seg.len - a.tokens + 1 || drop0 || drop1;
+        bool mend = false;
+        if (__builtin_expect(edge, 0)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool drop = u ? drop1 : drop0;
+                const int tu = t0 + u * kKvTile;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (t0 + r + 8 * (e >> 1) >= seen[nt][e & 1]) P[nt][e] = -INFINITY;
+                        if (drop || tu + r + 8 * (e >> 1) >= seen[nt][e & 1]) P[nt][u][e] = -INFINITY;
                 // places behind the sequence's end may hold anything
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int t = t0 + 8 * h + 2 * j;
-                        if (t >= at.len) vs[2 * g + h] = 0u;
-                        else if (t + 1 >= at.len) vs[2 * g + h] &= 0xFFFFu;
+                        const int t = tu + 8 * h + 2 * j;
+                        if (drop || t >= seg.len) vs[u][2 * g + h] = 0u;
+                        else if (t + 1 >= seg.len) vs[u][2 * g + h] &= 0xFFFFu;
                     }
             }
-            uint32_t any = 0;
+        }
+        uint32_t any = 0;
 #pragma unroll
-            for (int g = 0; g < 2 * G; ++g) any |= vs[g];
-            const bool large = (any & 0x40004000u) != 0u;                // a scale of 2 or more
-            const float sl = a.scale_log2 * 0x1p24f;
-            bool lift = large && off > 0.f;
+        for (int g = 0; g < 2 * G; ++g) any |= vs[0][g] | vs[1][g];
+        if (__builtin_expect(edge && __any_sync(0xffffffffu, (any & 0x40004000u) != 0u), 0)) {
+            // a token may be hidden from some columns only, and its scale be NaN (which the test above
+            // catches, among other large ones): nothing times NaN is nothing there
+            mend = true;
+        }
+        const bool large = (any & 0x40004000u) != 0u;                // a scale of 2 or more
+        bool lift = large && off > 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                lift |= fmaxf(fmaxf(P[nt][0][e], P[nt][0][e + 2]), fmaxf(P[nt][1][e], P[nt][1][e + 2])) > most[nt][e];
+        if (__any_sync(0xffffffffu, lift)) {
+            const float before = off;
+            if (__any_sync(0xffffffffu, large)) off = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    lift |= fmaxf(P[nt][e], P[nt][e + 2]) * sl > R[nt][e] + (off + kKvSlack);
-            if (__any_sync(0xffffffffu, lift)) {
-                const float before = off;
-                if (__any_sync(0xffffffffu, large)) off = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(fmaxf(P[nt][0][e], P[nt][0][e + 2]), fmaxf(P[nt][1][e], P[nt][1][e + 2])) * sl;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float ref = fmaxf(mx, R[nt][e] + before) - off;
+                    const float f = R[nt][e] == ref ? 1.f : kv_exp2(R[nt][e] - ref);
+                    R[nt][e] = ref;
+                    most[nt][e] = (ref + (off + kKvSlack)) * inv_sl;
+                    L[nt][e] *= f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(P[nt][e], P[nt][e + 2]) * sl;
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        const float ref = fmaxf(mx, R[nt][e] + before) - off;
-                        const float f = R[nt][e] == ref ? 1.f : kv_exp2(R[nt][e] - ref);
-                        R[nt][e] = ref;
-                        L[nt][e] *= f;
-#pragma unroll
-                        for (int m = 0; m < D / 16; ++m) {
-                            O[nt][m][e] *= f;
-                            O[nt][m][e + 2] *= f;
-                        }
+                    for (int m = 0; m < D / 16; ++m) {
+                        O[nt][m][e] *= f;
+                        O[nt][m][e + 2] *= f;
                     }
-            }
-            uint32_t pt[NT][2];
+                }
+        }
+        uint32_t pt[NT][2][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // a column that has seen nothing yet keeps R = -inf: its weights are 2^-inf = 0
-                const float r0 = R[nt][0] == -INFINITY ? 0.f : R[nt][0], r1 = R[nt][1] == -INFINITY ? 0.f : R[nt][1];
-                const float p0 = kv_exp2(fmaf(P[nt][0], sl, -r0)), p1 = kv_exp2(fmaf(P[nt][1], sl, -r1));
-                const float p2 = kv_exp2(fmaf(P[nt][2], sl, -r0)), p3 = kv_exp2(fmaf(P[nt][3], sl, -r1));
+        for (int nt = 0; nt < NT; ++nt) {
+            // a column that has seen nothing yet keeps R = -inf: its weights are 2^-inf = 0
+            const float r0 = R[nt][0] == -INFINITY ? 0.f : R[nt][0], r1 = R[nt][1] == -INFINITY ? 0.f : R[nt][1];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float p0 = kv_exp2(fmaf(P[nt][u][0], sl, -r0)), p1 = kv_exp2(fmaf(P[nt][u][1], sl, -r1));
+                const float p2 = kv_exp2(fmaf(P[nt][u][2], sl, -r0)), p3 = kv_exp2(fmaf(P[nt][u][3], sl, -r1));
                 L[nt][0] += p0 + p2;
                 L[nt][1] += p1 + p3;
-                pt[nt][0] = kv_transpose(h2_bits(__floats2half2_rn(p0, p1)));
-                pt[nt][1] = kv_transpose(h2_bits(__floats2half2_rn(p2, p3)));
+                pt[nt][u][0] = kv_transpose(h2_bits(__floats2half2_rn(p0, p1)));
+                pt[nt][u][1] = kv_transpose(h2_bits(__floats2half2_rn(p2, p3)));
             }
+        }
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                uint32_t w[2];
-                kv_lds<2>(w, tile + T::kV + (g * 64 + lane * 2) * 4);
-                uint32_t va[2][4];
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    va[u][0] = kv_value(w[u] & 0x000F000Fu, 0x1p14f);
-                    va[u][1] = kv_value(w[u] & 0x00F000F0u, 0x1p10f);
-                    va[u][2] = kv_value((w[u] >> 8) & 0x000F000Fu, 0x1p14f);
-                    va[u][3] = kv_value((w[u] >> 8) & 0x00F000F0u, 0x1p10f);
+            for (int u = 0; u < 2; ++u) {
+                uint32_t w[2], va[2][4];
+                kv_lds<2>(w, tile[u] + T::kV + (g * 64 + lane * 2) * 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t hi = w[i] >> 8;
+                    va[i][0] = kv_value(w[i] & 0x000F000Fu, kKvLow);
+                    va[i][1] = kv_value(w[i] & 0x00F000F0u, kKvHigh);
+                    va[i][2] = kv_value(hi & 0x000F000Fu, kKvLow);
+                    va[i][3] = kv_value(hi & 0x00F000F0u, kKvHigh);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t b0 = h2_bits(__hmul2(bits_h2(pt[nt][0]), bits_h2(vs[2 * g])));
-                    uint32_t b1 = h2_bits(__hmul2(bits_h2(pt[nt][1]), bits_h2(vs[2 * g + 1])));
-                    if (edge) {
-                        // a hidden token's scale may be NaN: nothing times NaN is nothing here
-                        b0 &= ~__vcmpeq2(pt[nt][0], 0u);
-                        b1 &= ~__vcmpeq2(pt[nt][1], 0u);
+                    uint32_t b0 = h2_bits(__hmul2(bits_h2(pt[nt][u][0]), bits_h2(vs[u][2 * g])));
+                    uint32_t b1 = h2_bits(__hmul2(bits_h2(pt[nt][u][1]), bits_h2(vs[u][2 * g + 1])));
+                    if (mend) {
+                        b0 = kv_hide(b0, pt[nt][u][0]);
+                        b1 = kv_hide(b1, pt[nt][u][1]);
                     }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float (&o)[4] = O[nt][2 * g + u];
-                        kv_mma(o, va[u][0], va[u][1], va[u][2], va[u][3], b0, b1, o[0], o[1], o[2], o[3]);
+                    for (int i = 0; i < 2; ++i) {
+                        float (&o)[4] = O[nt][2 * g + i];
+                        kv_mma(o, va[i][0], va[i][1], va[i][2], va[i][3], b0, b1, o[0], o[1], o[2], o[3]);
                     }
                 }
             }
-        }
         __syncwarp();                                                     // all lanes have read the stage
-        if (x + S < n && !dead) issue(s);
+        if (to_copy > 0 && !dead) issue(s);
+        if (++s == S) {
+            s = 0;
+            parity ^= 1u;
+        }
 
-        const bool ends = at.tile + 1 == at.tiles;
-        if (ends || x + 1 == n) {
+        const bool ends = seg.tile + step == seg.tiles;
+        if (ends || x + step == n) {
             const bool begins = seg_tile0 == 0;
             const bool whole = ends && begins;
             float *dst = nullptr;
@@ -500,9 +688,9 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                     const int c = nt * 8 + 2 * j + e;
-                    if (c >= kv_columns(a, at.hc, C::kCols)) continue;
+                    if (c >= kv_columns(a, seg.hc, C::kCols)) continue;
                     if (whole) {
-                        __half *row = kv_out_row(a, at.b, at.hc, c, C::kCols, D);
+                        __half *row = kv_out_row(a, seg.b, seg.hc, c, C::kCols, D);
                         const float inv = l == 0.f ? 0.f : 0x1p10f / l;
 #pragma unroll
                         for (int m = 0; m < D / 16; ++m) {
@@ -518,121 +706,119 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                         if (r == 0) {
                             dst[C::kCols * D + c] = R[nt][e];
                             dst[C::kCols * (D + 1) + c] = l;
+                            reinterpret_cast<int *>(dst)[C::kPart] = seg.b;
+                            reinterpret_cast<int *>(dst)[C::kPart + 1] = seg.hc;
                         }
                     }
                 }
             fresh = true;
         }
-        at.next(a);
+        seg.tile += step;
+        if (ends && x + step < n) seg.next_segment(ix);
     }
-    if (lane == 0) {
-        open[warp] = is_open;
-        began[warp] = did_begin;
-        first[warp] = did_first;
-    }
+    if (lane == 0) flags[warp] = (n > 0 ? 1 : 0) | (is_open ? 2 : 0) | (did_begin ? 4 : 0) | (did_first ? 8 : 0);
     __syncthreads();
 
-    // Join the segments that this CTA's warps share: the warp in which such a segment begins, or the
-    // first warp with tiles for one that began in an earlier CTA, walks on to where it ends.
-    if (n == 0) return;
-    KvCursor seg = {};
-    auto join = [&](int w_end, bool ends_here, bool began_here) {
-        // partials: this warp's tail (or, for a single partial, its head), the tails of the warps between, w_end's head or tail
+    // Join the segments that this CTA's warps share.  Each such segment is a chain of warps: it starts where
+    // the segment begins (or at the first warp with tiles, for one that began in an earlier CTA) and ends with
+    // the warp that wrote its end (or the last warp with tiles).  All warps see the chains alike and take
+    // their columns, 32 values at a time, in turn.
+    const int mine = lane < W ? flags[lane] : 0;
+    const unsigned some = __ballot_sync(0xffffffffu, mine & 1), opens = __ballot_sync(0xffffffffu, mine & 2),
+                   begins = __ballot_sync(0xffffffffu, mine & 4), ends = __ballot_sync(0xffffffffu, mine & 8);
+    const unsigned leader = some & (0u - some);
+    auto join = [&](int w0, int w1, bool ends_here, bool began_here, int &task) {
+        // w0's partial (its tail; its head, if it is the whole chain), the tails of the warps between, w1's
+        const unsigned in = some & (0xffffffffu >> (31 - w1)) & (0xffffffffu << w0);
+        auto part = [&](int w) {
+            return w == w1 && ends_here ? heads + w * (C::kPartBytes / 4)
+                                        : reinterpret_cast<const float *>(rings + w * C::kRing);
+        };
         float *out_part = a.part + ((long long)blockIdx.x * 2 + (ends_here ? 0 : 1)) * C::kPart;
-        for (int c = 0; c < kv_columns(a, seg.hc, C::kCols); ++c) {
-            float top = -INFINITY;
-            for (int w = warp; w <= w_end; ++w) {
-                if (w > warp && kv_run(c_hi - c_lo, w, W) == kv_run(c_hi - c_lo, w + 1, W)) continue;
-                const float *p = (w == w_end && ends_here) ? heads + w * (C::kPartBytes / 4)
-                                                           : reinterpret_cast<float *>(rings + w * C::kRing);
-                top = fmaxf(top, p[C::kCols * D + c]);
-            }
-            const float ref = top == -INFINITY ? 0.f : top;
-            float l = 0.f, acc[D / 32];
+        const int *id = reinterpret_cast<const int *>(part(w0)) + C::kPart;
+        const int seg_b = id[0], seg_hc = id[1];
+        const int tasks = kv_columns(a, seg_hc, C::kCols) * (D / 32);
+        for (int k = (warp + W - task % W) % W; k < tasks; k += W) {
+            const int c = k / (D / 32), e = k % (D / 32);
+            const bool has = (in >> lane) & 1u;
+            const float *p = part(has ? lane : w0);
+            const float R1 = has ? p[C::kCols * D + c] : -INFINITY;
+            float top = R1;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-            for (int w = warp; w <= w_end; ++w) {
-                if (w > warp && kv_run(c_hi - c_lo, w, W) == kv_run(c_hi - c_lo, w + 1, W)) continue;
-                const float *p = (w == w_end && ends_here) ? heads + w * (C::kPartBytes / 4)
-                                                           : reinterpret_cast<float *>(rings + w * C::kRing);
-                const float f = kv_exp2(p[C::kCols * D + c] - ref);
-                l += p[C::kCols * (D + 1) + c] * f;
+            for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float f = has ? kv_exp2(R1 - (top == -INFINITY ? 0.f : top)) : 0.f;
+            float l = has ? p[C::kCols * (D + 1) + c] * f : 0.f, acc = 0.f;
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc[e] += p[c * D + 32 * e + lane] * f;
+            for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll 4
+            for (int w = w0; w <= w1; ++w) {
+                // warps without tiles have weight 0; what their memory holds must not be multiplied with it
+                const float fw = __shfl_sync(0xffffffffu, f, w), v = part(w)[c * D + 32 * e + lane];
+                acc += (in >> w) & 1u ? v * fw : 0.f;
             }
             if (ends_here && began_here) {
-                __half *row = kv_out_row(a, seg.b, seg.hc, c, C::kCols, D);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) row[32 * e + lane] = __float2half_rn(acc[e] * inv);
+                kv_out_row(a, seg_b, seg_hc, c, C::kCols, D)[32 * e + lane] = __float2half_rn(l == 0.f ? 0.f : acc / l);
             } else {
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) out_part[c * D + 32 * e + lane] = acc[e];
-                if (lane == 0) {
+                out_part[c * D + 32 * e + lane] = acc;
+                if (e == 0 && lane == 0) {
                     out_part[C::kCols * D + c] = top;
                     out_part[C::kCols * (D + 1) + c] = l;
                 }
             }
         }
+        task += tasks;
     };
-    int w_first = 0;
-    while (kv_run(c_hi - c_lo, w_first, W) == kv_run(c_hi - c_lo, w_first + 1, W)) ++w_first;
-    if (warp == w_first && first[warp]) {
-        // the segment that came in from an earlier CTA ends in this warp
-        seg.seek(a, prefix, lo);
-        join(warp, true, false);
+    int task = 0;
+    if (ends & leader) {
+        const int w = __ffs(leader) - 1;      // a segment of an earlier CTA ends in the first warp
+        join(w, w, true, false, task);
     }
-    if (open[warp] && (began[warp] || warp == w_first)) {
-        seg.seek(a, prefix, hi - 1);
-        int w = warp;
-        bool ends_here = false;
-        while (w + 1 < W) {
-            ++w;
-            if (kv_run(c_hi - c_lo, w, W) == kv_run(c_hi - c_lo, w + 1, W)) continue;
-            if (first[w]) {
-                ends_here = true;
-                break;
-            }
-        }
-        join(w, ends_here, began[warp]);
+    for (unsigned left = opens & (begins | leader); left; left &= left - 1) {
+        const int w0 = __ffs(left) - 1;
+        const unsigned beyond = w0 < 31 ? 0xffffffffu << (w0 + 1) : 0u, end = ends & beyond;
+        join(w0, end ? __ffs(end) - 1 : 31 - __clz(some), end != 0, (begins >> w0) & 1u, task);
     }
 }
 
-// One CTA per (segment, column): joins what CTAs of the main kernel left of a
-// segment they share, in order; writes zeros for a sequence without tokens.
+// One CTA per (cut between two runs, column): if the cut is the first within its
+// segment, joins what the main kernel's CTAs left of that segment, in order.  The
+// main kernel lets it start after its own wait, so the lengths are there.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a)
 {
     using C = KvAttnCfg<D, NT>;
-    extern __shared__ int kv_join_prefix[];
+    extern __shared__ int kv_join_index[];
+    __shared__ float weight[kKvMaxCtas], sums[kKvMaxCtas];
+    KvIndex ix;
+    ix.build(a, kv_join_index);
+    const int total = ix.total(), n_ctas = kv_ctas(total, a.ctas, C::kWarps), cut = blockIdx.x + 1, c = blockIdx.y,
+              d = threadIdx.x;
+    const KvRuns runs(total, n_ctas);
+    const int x = runs.start(min(cut, n_ctas - 1));
+    KvCursor seg;
+    seg.seek(ix, x);
+    // every CTA waits: when this kernel is done, so must the main one be for what follows on the stream
     kv_pdl_wait();
-    kv_prefix(a, kv_join_prefix);
-    const int total = kv_join_prefix[a.at.n_seqs];
-    const int per = a.at.kv_heads * a.blocks;
-    const int b = blockIdx.x / per, hc = blockIdx.x - b * per, c = blockIdx.y, d = threadIdx.x;
-    if (c >= kv_columns(a, hc, C::kCols) || d >= D) return;
-    __half *row = kv_out_row(a, b, hc, c, C::kCols, D);
-    const int tiles = (kv_join_prefix[b + 1] - kv_join_prefix[b]) / per;
-    if (tiles == 0) {
-        row[d] = __float2half_rn(0.f);
-        return;
+    if (cut >= n_ctas || seg.tile == 0 || seg.tile >= seg.tiles || c >= kv_columns(a, seg.hc, C::kCols)) return;
+    const int x0 = x - seg.tile, f = runs.owner(x0), n = runs.owner(x0 + seg.tiles - 1) - f + 1;
+    if (f != cut - 1) return;
+    auto part = [&](int i) { return a.part + ((long long)(f + i) * 2 + (i == n - 1 ? 0 : 1)) * C::kPart; };
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        weight[i] = part(i)[C::kCols * D + c];
+        sums[i] = part(i)[C::kCols * (D + 1) + c];
     }
-    const int n_ctas = kv_ctas(total, a.ctas, C::kWarps);
-    const int x0 = kv_join_prefix[b] + hc * tiles, x1 = x0 + tiles;
-    const int f = kv_owner(total, x0, n_ctas), l = kv_owner(total, x1 - 1, n_ctas);
-    if (f == l) return;                            // one CTA had it all
-    auto part = [&](int cta) { return a.part + ((long long)cta * 2 + (cta == l ? 0 : 1)) * C::kPart; };
-    float top = -INFINITY;
-    for (int i = f; i <= l; ++i) top = fmaxf(top, part(i)[C::kCols * D + c]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc = 0.f;
-    for (int i = f; i <= l; ++i) {
-        const float *p = part(i);
-        const float w = kv_exp2(p[C::kCols * D + c] - ref);
-        sum += p[C::kCols * (D + 1) + c] * w;
-        acc += p[c * D + d] * w;
+    __syncthreads();
+    float top = -INFINITY, sum = 0.f, acc = 0.f;
+    for (int i = 0; i < n; ++i) top = fmaxf(top, weight[i]);
+    if (top == -INFINITY) top = 0.f;
+    if (d >= D) return;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float w = kv_exp2(weight[i] - top);
+        sum += sums[i] * w;
+        acc += part(i)[c * D + d] * w;
     }
-    row[d] = __float2half_rn(sum == 0.f ? 0.f : acc / sum);
+    kv_out_row(a, seg.b, seg.hc, c, C::kCols, D)[d] = __float2half_rn(sum == 0.f ? 0.f : acc / sum);
 }
 
 }  // namespace zt

@@ -20,7 +20,6 @@ namespace {
 using namespace zt;
 
 constexpr int kRowsMax = 1 << 24;
-constexpr int kSmsB200 = 148;      // sizes the workspace, so that the query needs no device
 
 int device_error(cudaError_t e, int status)
 {
@@ -110,17 +109,21 @@ int launch(void (*fn)(Args), dim3 grid, int threads, size_t smem, const Args &ar
 dim3 row_grid(int rows, int items)
 {
     const int most = std::max(1, (items + 255) / 256);
-    return dim3((unsigned)rows, (unsigned)std::max(1, std::min(most, 2 * kSmsB200 / std::max(1, rows) + 1)));
+    return dim3((unsigned)rows, (unsigned)std::max(1, std::min(most, 2 * 148 / std::max(1, rows) + 1)));
 }
 
 size_t part_bytes(int head_dim, int cols8)
 {
-    return (size_t)kSmsB200 * 2 * cols8 * (head_dim + 2) * sizeof(float);
+    return (size_t)kKvMaxCtas * 2 * cols8 * (head_dim + 2) * sizeof(float);
 }
 
 // Columns (query tokens x grouped heads) go through the matrix instruction eight at a time; from nine
 // on, sixteen share one pass over the cache.
 int column_tiles(int cols) { return cols > 8 ? 2 : 1; }
+
+// Segments of at most this many tokens (as far as the page table reaches), one wave of them: a CTA's 16
+// warps take one each, without a second launch.
+constexpr int kWholeTokens = 1024;
 
 template <int D, int NT>
 int launch_attention(KvAttnArgs &a, void *stream)
@@ -128,15 +131,18 @@ int launch_attention(KvAttnArgs &a, void *stream)
     using C = KvAttnCfg<D, NT>;
     a.blocks = (a.cols + C::kCols - 1) / C::kCols;
     const int64_t segments = (int64_t)a.at.n_seqs * a.at.kv_heads * a.blocks;
-    if (segments * a.at.max_pages * (a.at.page_size / kKvTile) > INT_MAX) return ZT_ERR_UNSUPPORTED;
-    const size_t prefix = ((size_t)a.at.n_seqs + 1) * sizeof(int);
+    if (segments * ((int64_t)a.at.max_pages * (a.at.page_size / kKvTile) + kKvSegTiles) > INT_MAX) return ZT_ERR_UNSUPPORTED;
+    const size_t index = (2 * (size_t)a.at.n_seqs + 1) * sizeof(int);
     int sms = 0;
-    if (resident_ctas(reinterpret_cast<const void *>(&kv_attn_kernel<D, NT>), C::kWarps * 32, C::kSmem + prefix, sms) < 1)
+    if (resident_ctas(reinterpret_cast<const void *>(&kv_attn_kernel<D, NT>), C::kWarps * 32, C::kSmem + index, sms) < 1)
         return ZT_ERR_DEVICE;
-    a.ctas = std::min(sms, kSmsB200);
-    int rc = launch(kv_attn_kernel<D, NT>, dim3((unsigned)a.ctas), C::kWarps * 32, C::kSmem + prefix, a, stream);
-    if (rc) return rc;
-    return launch(kv_attn_join_kernel<D, NT>, dim3((unsigned)segments, (unsigned)std::min(C::kCols, a.cols)), 128, prefix,
+    const int longest = a.at.max_pages * a.at.page_size;
+    a.whole = segments <= sms && longest <= kWholeTokens * C::kWarps / 16;
+    a.ctas = a.whole ? (int)segments : std::min(sms, kKvMaxCtas);
+    const int rc = launch(kv_attn_kernel<D, NT>, dim3((unsigned)a.ctas), C::kWarps * 32, C::kSmem + index, a, stream);
+    if (rc || a.whole) return rc;
+    if (a.ctas == 1) return ZT_OK;
+    return launch(kv_attn_join_kernel<D, NT>, dim3((unsigned)a.ctas - 1, (unsigned)std::min(C::kCols, a.cols)), 128, index,
                   a, stream);
 }
 

@@ -507,7 +507,7 @@ class Pass:
 # ----------------------------------------------- paged 4-bit KV cache --
 ZT_Q4_KV_ERR_PLACE = 1
 ZT_Q4_KV_ERR_WAIT = 2
-ZT_Q4_KV_MAX_SEQS = 4096
+ZT_Q4_KV_MAX_SEQS = 2048
 
 
 def kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -560,7 +560,8 @@ class _Launch:
     def _launch(self, stream):
         torch = _torch()
         if stream is None:
-            stream = torch.cuda.current_stream(self._device).cuda_stream
+            # the raw handle: building torch's Stream object takes longer than a launch
+            stream = torch._C._cuda_getCurrentRawStream(self._device.index)
         else:
             stream = _stream_handle(stream)
         _check(self._fn(*self._args, stream), self._name)

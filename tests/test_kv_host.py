@@ -118,12 +118,12 @@ def test_attention_refusals(zt):
     for bad, name in ((dict(q=None), "INVALID_ARG"), (dict(ld_q=504), "INVALID_ARG"), (dict(ld_q=516), "MISALIGNED"),
                       (dict(q=FAKE + 8), "MISALIGNED"), (dict(heads=7), "INVALID_ARG"), (dict(heads=0), "INVALID_ARG"),
                       (dict(tokens=0), "INVALID_ARG"), (dict(tokens=17), "INVALID_ARG"), (dict(lens=None), "INVALID_ARG"),
-                      (dict(table=None), "INVALID_ARG"), (dict(seqs=0), "INVALID_ARG"), (dict(seqs=4097), "INVALID_ARG"),
+                      (dict(table=None), "INVALID_ARG"), (dict(seqs=0), "INVALID_ARG"), (dict(seqs=2049), "INVALID_ARG"),
                       (dict(max_pages=0), "INVALID_ARG"), (dict(scale=0.0), "INVALID_ARG"), (dict(scale=-1.0), "INVALID_ARG"),
                       (dict(scale=float("nan")), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG"),
                       (dict(out=None), "INVALID_ARG"), (dict(out=FAKE + 1), "MISALIGNED"), (dict(ld=511), "INVALID_ARG"),
                       (dict(work=None), "INVALID_ARG"), (dict(work=FAKE + 8), "MISALIGNED"), (dict(nbytes=ws - 1), "WORKSPACE"),
-                      (dict(seqs=4096, max_pages=2**18), "UNSUPPORTED")):
+                      (dict(seqs=2048, max_pages=2**19), "UNSUPPORTED")):
         assert call(**bad) == status(zt, name), bad
 
 
@@ -138,7 +138,7 @@ def test_prompt_refusals(zt):
                       (dict(ld=504), "INVALID_ARG"), (dict(ld_q=516), "MISALIGNED"), (dict(ld_k=132), "MISALIGNED"),
                       (dict(q=FAKE + 8), "MISALIGNED"), (dict(out=FAKE + 2), "MISALIGNED"), (dict(v=FAKE + 4), "MISALIGNED"),
                       (dict(cu_q=FAKE + 2), "MISALIGNED"), (dict(err=FAKE + 2), "MISALIGNED"), (dict(seqs=0), "INVALID_ARG"),
-                      (dict(seqs=4097), "INVALID_ARG"), (dict(total_q=-1), "INVALID_ARG"), (dict(total_k=2**25), "INVALID_ARG"),
+                      (dict(seqs=2049), "INVALID_ARG"), (dict(total_q=-1), "INVALID_ARG"), (dict(total_k=2**25), "INVALID_ARG"),
                       (dict(heads=7), "INVALID_ARG"), (dict(kv_heads=0), "INVALID_ARG"), (dict(heads=1), "INVALID_ARG"),
                       (dict(dim=80), "UNSUPPORTED"), (dict(dim=256), "UNSUPPORTED"), (dict(causal=2), "INVALID_ARG"),
                       (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG")):
