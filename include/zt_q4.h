@@ -411,6 +411,7 @@ ZT_API int zt_q4_gemm_f16w_gate_up_silu(const uint16_t *w16, const uint16_t *x, 
  */
 #define ZT_Q4_KV_ERR_PLACE 1u
 #define ZT_Q4_KV_ERR_WAIT 2u
+#define ZT_Q4_KV_ERR_WORKSPACE 4u
 #define ZT_Q4_KV_MAX_SEQS 2048
 
 typedef struct zt_q4_kv {
@@ -482,8 +483,11 @@ ZT_API int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int
  * Scores, softmax statistics and sums are fp32; the weights are rounded to fp16
  * before and after they are multiplied by V's scales.
  * workspace: DEVICE, 16-byte aligned, zt_q4_kv_attention_workspace_bytes() bytes
- * (a function of these sizes alone); contents on entry do not matter.  Calls that
- * may overlap need workspaces of their own.  One or two launches.
+ * (a function of these sizes alone).  Unlike the other workspaces of this library
+ * it must be ZERO-FILLED before its first use: it holds counters that every call
+ * leaves at zero again, for calls of any sizes.  (Otherwise outputs may be missing;
+ * bit 2, ZT_Q4_KV_ERR_WORKSPACE, of *err reports what the kernel can tell.)  Calls
+ * that may overlap need workspaces of their own.  One launch.
  */
 ZT_API size_t zt_q4_kv_attention_workspace_bytes(int kv_heads, int q_heads, int head_dim, int tokens);
 ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, int q_heads, int tokens,

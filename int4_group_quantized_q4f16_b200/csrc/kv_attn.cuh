@@ -22,22 +22,22 @@
 // tcgen05 would need the unpacked codes written to shared memory first (4x the
 // cache's bytes); the work is bound by the cache's bytes.
 //
-// R is a reference, not the running maximum: p may exceed 2^kOff.., so O and the
-// sum of p are rescaled only when a score passes R by kOff + 2.  kOff keeps p * vs in
-// the upper range of fp16: with scales below 2 (values below 14) p * vs stays
-// under 2^15, and a weight of 2^-26 of the largest one still has 3 bits.  A tile
-// with a larger scale sets the offset to 0 (p <= 4, p * vs <= 4 * 65504 / 7).
-// p is rounded to fp16, p * vs once more; sums of p and O are fp32.
+// R is a reference, not the running maximum: the largest score when it was set, less
+// 9 (p = 2^9 there).  O and the sum of p are rescaled only when a score passes R by
+// 15.  That keeps p * vs in the upper range of fp16: with scales below 2 (values
+// below 14) p * vs stays under 2^16, and a weight of 2^-24 of the largest one still
+// has 2 bits.  A tile with a larger scale sets the two to 0 and 2 (p <= 4, p * vs <=
+// 4 * 65504 / 7).  p is rounded to fp16, p * vs once more; sums of p and O are fp32.
 //
 // Work split.  The (sequence, kv head) segments are laid end to end in tiles, each
 // with two more that stand for its own cost, and cut into equal runs, one per CTA,
 // then one per warp: ragged batches and single long sequences balance alike.  Each
 // warp streams its run through a private ring of bulk copies (a tile is K and V),
 // two tiles at a time.  Where every segment is short and there are few of them, a
-// CTA takes one whole segment and the second launch is saved.  Segments cut between
-// warps are joined in shared memory, segments cut between CTAs by
-// kv_attn_join_kernel, always in the order of the tokens: results do not depend on
-// timing.
+// CTA takes one whole segment.  Segments cut between warps are joined in shared
+// memory; of the CTAs that share a segment each leaves its part in the workspace and
+// counts itself, and the one that counts last joins them.  Both joins go in the
+// order of the tokens: results do not depend on timing.
 #pragma once
 
 #include "kv_common.cuh"
@@ -49,13 +49,13 @@ struct KvAttnArgs {
     const __half *q;
     __half *out;
     const int32_t *lens;
+    unsigned int *arrived;     // [kKvMaxCtas] zero between calls: partials of a cut segment, counted at its first CTA
     float *part;               // partial results of segments cut between CTAs
     long long ld_q, ld_out;    // elements between query tokens
     int tokens;                // query tokens per sequence
     int q_heads, group;        // group = q_heads / kv_heads
     int cols, blocks;          // columns of a kv head (tokens * group), and blocks of 8 NT of them
-    int ctas;                  // CTAs of the main kernel
-    int whole;                 // 1: a CTA takes one whole segment, nothing is left to join
+    int whole;                 // 1: a CTA takes one whole segment
     float scale_log2;          // softmax scale * log2(e)
 };
 
@@ -71,14 +71,14 @@ struct KvAttnCfg {
     static constexpr int kPartBytes = (kPart * 4 + 8 + 15) / 16 * 16;         // and the segment, within a CTA
     static_assert(kPartBytes <= kRing, "a warp's last partial goes to its ring");
     static constexpr int kBars = kWarps * kPairs * 8;
-    static constexpr int kFlags = kWarps * 4;
+    static constexpr int kFlags = kWarps * (4 + 16) + 32;
     static constexpr int kSmem = kWarps * (kRing + kPartBytes) + kBars + kFlags;   // + KvIndex, 8 bytes per sequence
 };
 
 constexpr int kKvSegTiles = 2;         // what starting and ending a segment costs, in tiles
 constexpr int kKvWarpTiles = 1;        // tiles per warp below which fewer CTAs are used
 constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
-constexpr float kKvOff = 12.f, kKvSlack = 2.f;
+constexpr float kKvOff = 9.f, kKvRoom = 15.f, kKvRoomLarge = 2.f;
 
 // Runs of tiles: CTA c of n takes total / n of them, the first total % n CTAs one more.
 struct KvRuns {
@@ -248,14 +248,14 @@ static __device__ __noinline__ uint32_t kv_hide(uint32_t b, uint32_t p) { return
 // Columns of head-and-block hc.
 __device__ __forceinline__ int kv_columns(const KvAttnArgs &a, int hc, int kcols)
 {
-    return min(kcols, a.cols - hc % a.blocks * kcols);
+    return a.blocks == 1 ? a.cols : min(kcols, a.cols - hc % a.blocks * kcols);
 }
 
 // Row of the output for column c of (b, hc).
 __device__ __forceinline__ __half *kv_out_row(const KvAttnArgs &a, int b, int hc, int c, int kcols, int D)
 {
-    const int h = hc / a.blocks, col = (hc - h * a.blocks) * kcols + c;
-    const int i = col / a.group, head = h * a.group + (col - i * a.group);
+    const int h = a.blocks == 1 ? hc : hc / a.blocks, col = (hc - h * a.blocks) * kcols + c;
+    const int i = a.tokens == 1 ? 0 : col / a.group, head = h * a.group + (col - i * a.group);
     return a.out + ((long long)b * a.tokens + i) * a.ld_out + head * D;
 }
 
@@ -264,6 +264,17 @@ __device__ __forceinline__ void kv_zero(const KvAttnArgs &a, int b, int hc, int 
 {
     for (int i = threadIdx.x; i < kv_columns(a, hc, kcols) * D; i += blockDim.x)
         kv_out_row(a, b, hc, i / D, kcols, D)[i % D] = __float2half_rn(0.f);
+}
+
+// A part of a segment that other CTAs share, left in the workspace: value d of column c.
+template <typename C>
+__device__ __forceinline__ void kv_leave(float *part, int c, int d, float top, float l, float acc, int D)
+{
+    part[c * D + d] = acc;
+    if (d == 0) {
+        part[C::kCols * D + c] = top;
+        part[C::kCols * (D + 1) + c] = l;
+    }
 }
 
 template <int D, int NT>
@@ -278,28 +289,31 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
     const uint32_t bars = kv_smem(kv_smem_raw) + W * (C::kRing + C::kPartBytes);
     int *index = reinterpret_cast<int *>(kv_smem_raw + C::kSmem);
     // all shared memory is dynamic: the opt-in limit leaves no room for a static part
-    int *flags = index - W;          // of each warp: 1 it had tiles, 2 its last segment goes on in the next warp,
+    int4 *starts = reinterpret_cast<int4 *>(index) - W;     // of each warp's run: sequence, head-and-block, tile, tiles
+    int4 *chains = starts - 2;       // the segments cut at the run's start and at its end: first CTA (-1: none),
+                                     // number of CTAs, sequence, head-and-block
+    int *flags = reinterpret_cast<int *>(chains) - W;
+                                     // of each warp: 1 it had tiles, 2 its last segment goes on in the next warp,
                                      // 4 and began in it, 8 it wrote the end of a segment that began earlier
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
     const uint32_t ring = kv_smem(rings) + warp * C::kRing, bar = bars + 8 * warp * S;
     if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8 * lane) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    kv_pdl_launch();
     kv_pdl_wait();
-    kv_pdl_launch();                 // now the joining kernel may read the lengths too while this one runs
 
     // this CTA's run of tiles: its share of all of them, or one whole segment
     KvIndex ix;
-    KvCursor at = {}, seg = {};
-    int c_lo = 0, c_n;
+    KvCursor at = {};
     if (a.whole) {
         const int per = a.at.kv_heads * a.blocks;
         at.b = blockIdx.x / per;
         at.hc = blockIdx.x - at.b * per;
         at.len = kv_len(a, at.b);
-        at.tiles = c_n = (at.len + kKvTile - 1) / kKvTile;
+        at.tiles = (at.len + kKvTile - 1) / kKvTile;
         __syncwarp();
-        if (c_n == 0) {
+        if (at.tiles == 0) {
             kv_zero(a, at.b, at.hc, C::kCols, D);
             return;
         }
@@ -310,26 +324,47 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                 for (int hc = 0; hc < ix.per; ++hc) kv_zero(a, b, hc, C::kCols, D);
         const int total = ix.total(), n_ctas = kv_ctas(total, gridDim.x, W);
         if ((int)blockIdx.x >= n_ctas) return;
-        const KvRuns runs(total, n_ctas);
-        c_lo = runs.start(blockIdx.x);
-        c_n = runs.start(blockIdx.x + 1) - c_lo;
-    }
-    // this warp's run within it: n tiles from seg on
-    int lo = (int)((long long)c_n * warp / W), hi = (int)((long long)c_n * (warp + 1) / W), n = hi - lo;
-    if (a.whole) {
-        seg = at;
-        seg.tile = lo;
-    } else {
-        lo += c_lo;
-        hi += c_lo;
-        int upto = ix.total() - kKvSegTiles * ix.n * ix.per;
-        if (hi < ix.total()) {
-            seg.seek(ix, hi);
-            upto = seg.before(ix, hi);
+        if (warp == 0) {
+            // lane w finds where warp w's run starts (lane W: where the last one ends)
+            const KvRuns runs(total, n_ctas);
+            const int c_lo = runs.start(blockIdx.x), c_n = runs.start(blockIdx.x + 1) - c_lo;
+            const int x = c_lo + (int)((long long)c_n * min(lane, W) / W);
+            KvCursor c = {};
+            int before = total - kKvSegTiles * ix.n * ix.per;
+            if (x < total) {
+                c.seek(ix, x);
+                before = c.before(ix, x);
+            }
+            // the segments that this run's start and end cut: their first CTA, and how many share them
+            if (lane == 0 || lane == W) {
+                int4 chain = make_int4(-1, 0, c.b, c.hc);
+                if (x < total && c.tile > 0 && c.tile < c.tiles) {
+                    chain.x = runs.owner(x - c.tile);
+                    chain.y = runs.owner(x - c.tile + c.tiles - 1) - chain.x + 1;
+                }
+                chains[lane == W] = chain;
+            }
+            const int here = __shfl_down_sync(0xffffffffu, before, 1) - before;
+            if (lane < W) {
+                if (here > 0 && c.tile >= c.tiles) c.next_segment(ix);
+                starts[lane] = make_int4(c.b, c.hc, c.tile, here);
+            }
         }
-        seg.seek(ix, lo);
-        n = upto - seg.before(ix, lo);
-        if (n > 0 && seg.tile >= seg.tiles) seg.next_segment(ix);
+        __syncthreads();
+    }
+    // this warp's run: n tiles from seg on
+    KvCursor seg = at;
+    int n;
+    if (a.whole) {
+        seg.tile = at.tiles * warp / W;
+        n = at.tiles * (warp + 1) / W - seg.tile;
+    } else {
+        const int4 s = starts[warp];
+        seg.b = s.x;
+        seg.hc = s.y;
+        seg.tile = s.z;
+        n = s.w;
+        if (n > 0) seg.enter(ix);
     }
 
     float *tail = reinterpret_cast<float *>(rings + warp * C::kRing);
@@ -356,12 +391,15 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                    : nullptr;
         if (!fine && lane == 0) kv_error(a.at.err, kErrKvPlace);
     };
+    // a step reads the cache once: it should not push out of L2 what is read again, this kernel's code first of all
+    uint64_t once;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     auto copy = [&](int s, int u, int tiles) {      // `tiles` tiles from src on, to place u of stage s
         if (lane == 0 && src)
             asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                    ring + s * C::kStage + u * T::kBytes),
-                "l"(src), "r"(tiles * T::kBytes), "r"(bar + 8 * s) : "memory");
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
+                    "r"(ring + s * C::kStage + u * T::kBytes),
+                "l"(src), "r"(tiles * T::kBytes), "r"(bar + 8 * s), "l"(once) : "memory");
     };
     auto expect = [&](int s, int tiles) {           // a stage's arrival: the bytes of this many tiles
         if (lane == 0) {
@@ -606,7 +644,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                     const float ref = fmaxf(mx, R[nt][e] + before) - off;
                     const float f = R[nt][e] == ref ? 1.f : kv_exp2(R[nt][e] - ref);
                     R[nt][e] = ref;
-                    most[nt][e] = (ref + (off + kKvSlack)) * inv_sl;
+                    most[nt][e] = (ref + (off > 0.f ? kKvRoom : kKvRoomLarge)) * inv_sl;
                     L[nt][e] *= f;
 #pragma unroll
                     for (int m = 0; m < D / 16; ++m) {
@@ -719,106 +757,122 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
     if (lane == 0) flags[warp] = (n > 0 ? 1 : 0) | (is_open ? 2 : 0) | (did_begin ? 4 : 0) | (did_first ? 8 : 0);
     __syncthreads();
 
-    // Join the segments that this CTA's warps share.  Each such segment is a chain of warps: it starts where
-    // the segment begins (or at the first warp with tiles, for one that began in an earlier CTA) and ends with
-    // the warp that wrote its end (or the last warp with tiles).  All warps see the chains alike and take
-    // their columns, 32 values at a time, in turn.
+    // Join the segments that this CTA's warps share.  Each is a chain of warps: it starts where the segment begins
+    // (or at the first warp with tiles, for one that began in an earlier CTA) and ends with the warp that wrote its
+    // end (or the last warp with tiles).  All warps see the chains alike and take their columns, 32 values at a
+    // time, in turn; a lane weighs all partials by itself, which is shorter than any exchange.
     const int mine = lane < W ? flags[lane] : 0;
     const unsigned some = __ballot_sync(0xffffffffu, mine & 1), opens = __ballot_sync(0xffffffffu, mine & 2),
                    begins = __ballot_sync(0xffffffffu, mine & 4), ends = __ballot_sync(0xffffffffu, mine & 8);
     const unsigned leader = some & (0u - some);
-    auto join = [&](int w0, int w1, bool ends_here, bool began_here, int &task) {
+    unsigned left = opens & (begins | leader);
+    bool came = (ends & leader) != 0u;            // a segment of an earlier CTA ends in the first warp
+    const uint32_t tails_s = kv_smem(rings), heads_s = kv_smem(heads);
+#pragma unroll 1
+    for (int task = warp; came || left;) {
         // w0's partial (its tail; its head, if it is the whole chain), the tails of the warps between, w1's
-        const unsigned in = some & (0xffffffffu >> (31 - w1)) & (0xffffffffu << w0);
+        const int w0 = __ffs(came ? leader : left) - 1;
+        const unsigned end = came ? leader : ends & ~((2u << w0) - 1u);
+        const int w1 = end ? __ffs(end) - 1 : 31 - __clz(some);
+        const bool ends_here = end != 0u, whole = ends_here && !came && ((begins >> w0) & 1u);
+        const unsigned in = some & ((2u << w1) - 1u) & ~((1u << w0) - 1u);
+        if (came) came = false;
+        else left &= left - 1;
         auto part = [&](int w) {
-            return w == w1 && ends_here ? heads + w * (C::kPartBytes / 4)
-                                        : reinterpret_cast<const float *>(rings + w * C::kRing);
+            return w == w1 && ends_here ? heads_s + w * C::kPartBytes : tails_s + w * C::kRing;
         };
-        float *out_part = a.part + ((long long)blockIdx.x * 2 + (ends_here ? 0 : 1)) * C::kPart;
-        const int *id = reinterpret_cast<const int *>(part(w0)) + C::kPart;
-        const int seg_b = id[0], seg_hc = id[1];
-        const int tasks = kv_columns(a, seg_hc, C::kCols) * (D / 32);
-        for (int k = (warp + W - task % W) % W; k < tasks; k += W) {
-            const int c = k / (D / 32), e = k % (D / 32);
-            const bool has = (in >> lane) & 1u;
-            const float *p = part(has ? lane : w0);
-            const float R1 = has ? p[C::kCols * D + c] : -INFINITY;
-            float top = R1;
+        int b, hc;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b), "=r"(hc) : "r"(part(w0) + C::kPart * 4));
+        const int tasks = kv_columns(a, hc, C::kCols) * (D / 32);
+#pragma unroll 1
+        for (; task < tasks; task += W) {
+            const int c = task / (D / 32), d = task % (D / 32) * 32 + lane;
+            float f[W], v[W], top = -INFINITY, l = 0.f, acc = 0.f;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float f = has ? kv_exp2(R1 - (top == -INFINITY ? 0.f : top)) : 0.f;
-            float l = has ? p[C::kCols * (D + 1) + c] * f : 0.f, acc = 0.f;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll 4
-            for (int w = w0; w <= w1; ++w) {
-                // warps without tiles have weight 0; what their memory holds must not be multiplied with it
-                const float fw = __shfl_sync(0xffffffffu, f, w), v = part(w)[c * D + 32 * e + lane];
-                acc += (in >> w) & 1u ? v * fw : 0.f;
-            }
-            if (ends_here && began_here) {
-                kv_out_row(a, seg_b, seg_hc, c, C::kCols, D)[32 * e + lane] = __float2half_rn(l == 0.f ? 0.f : acc / l);
-            } else {
-                out_part[c * D + 32 * e + lane] = acc;
-                if (e == 0 && lane == 0) {
-                    out_part[C::kCols * D + c] = top;
-                    out_part[C::kCols * (D + 1) + c] = l;
+            for (int w = 0; w < W; ++w) {
+                f[w] = -INFINITY;
+                v[w] = 0.f;
+                if ((in >> w) & 1u) {
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[w]) : "r"(part(w) + (C::kCols * D + c) * 4));
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[w]) : "r"(part(w) + (c * D + d) * 4));
                 }
+                top = fmaxf(top, f[w]);
             }
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                f[w] = kv_exp2(f[w] - ref);
+                acc += v[w] * f[w];
+                v[w] = 0.f;
+                if ((in >> w) & 1u)
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[w]) : "r"(part(w) + (C::kCols * (D + 1) + c) * 4));
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) l += v[w] * f[w];
+            if (whole) kv_out_row(a, b, hc, c, C::kCols, D)[d] = __float2half_rn(l == 0.f ? 0.f : acc / l);
+            else kv_leave<C>(a.part + (2ll * blockIdx.x + (ends_here ? 0 : 1)) * C::kPart, c, d, top, l, acc, D);
         }
-        task += tasks;
-    };
-    int task = 0;
-    if (ends & leader) {
-        const int w = __ffs(leader) - 1;      // a segment of an earlier CTA ends in the first warp
-        join(w, w, true, false, task);
+        task -= tasks;                            // the next chain's tasks follow on
+        if (task < 0) task += W;
     }
-    for (unsigned left = opens & (begins | leader); left; left &= left - 1) {
-        const int w0 = __ffs(left) - 1;
-        const unsigned beyond = w0 < 31 ? 0xffffffffu << (w0 + 1) : 0u, end = ends & beyond;
-        join(w0, end ? __ffs(end) - 1 : 31 - __clz(some), end != 0, (begins >> w0) & 1u, task);
-    }
-}
+    if (a.whole) return;
 
-// One CTA per (cut between two runs, column): if the cut is the first within its
-// segment, joins what the main kernel's CTAs left of that segment, in order.  The
-// main kernel lets it start after its own wait, so the lengths are there.
-template <int D, int NT>
-__global__ void __launch_bounds__(128) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a)
-{
-    using C = KvAttnCfg<D, NT>;
-    extern __shared__ int kv_join_index[];
-    __shared__ float weight[kKvMaxCtas], sums[kKvMaxCtas];
-    KvIndex ix;
-    ix.build(a, kv_join_index);
-    const int total = ix.total(), n_ctas = kv_ctas(total, a.ctas, C::kWarps), cut = blockIdx.x + 1, c = blockIdx.y,
-              d = threadIdx.x;
-    const KvRuns runs(total, n_ctas);
-    const int x = runs.start(min(cut, n_ctas - 1));
-    KvCursor seg;
-    seg.seek(ix, x);
-    // every CTA waits: when this kernel is done, so must the main one be for what follows on the stream
-    kv_pdl_wait();
-    if (cut >= n_ctas || seg.tile == 0 || seg.tile >= seg.tiles || c >= kv_columns(a, seg.hc, C::kCols)) return;
-    const int x0 = x - seg.tile, f = runs.owner(x0), n = runs.owner(x0 + seg.tiles - 1) - f + 1;
-    if (f != cut - 1) return;
-    auto part = [&](int i) { return a.part + ((long long)(f + i) * 2 + (i == n - 1 ? 0 : 1)) * C::kPart; };
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        weight[i] = part(i)[C::kCols * D + c];
-        sums[i] = part(i)[C::kCols * (D + 1) + c];
+    // Parts left in the workspace: the CTA that counts last for a segment joins them.
+    if (chains[0].x < 0 && chains[1].x < 0) return;
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        // a segment that covers the whole run is cut at both ends, but left one part
+        const int f = chains[threadIdx.x].x, parts = chains[threadIdx.x].y;
+        bool joins = false;
+        if (f >= 0 && (threadIdx.x == 1 || f != chains[1].x)) {
+            __threadfence();
+            const unsigned before = atomicAdd(a.arrived + f, 1u);
+            joins = before == (unsigned)(parts - 1);
+            if (joins) a.arrived[f] = 0u;                   // for the next call
+            else if (before >= (unsigned)parts) kv_error(a.at.err, kErrKvWork);
+            __threadfence();
+        }
+        flags[threadIdx.x] = joins;
     }
     __syncthreads();
-    float top = -INFINITY, sum = 0.f, acc = 0.f;
-    for (int i = 0; i < n; ++i) top = fmaxf(top, weight[i]);
-    if (top == -INFINITY) top = 0.f;
-    if (d >= D) return;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float w = kv_exp2(weight[i] - top);
-        sum += sums[i] * w;
-        acc += part(i)[c * D + d] * w;
+    for (int k = 0; k < 2; ++k) {
+        if (!flags[k]) continue;
+        const int4 chain = chains[k];
+        const int parts = chain.y, tasks = kv_columns(a, chain.w, C::kCols) * (D / 32);
+        const float *base = a.part + (2ll * chain.x + 1) * C::kPart;      // the last part lies one slot earlier
+        auto at = [&](int i) { return (2 * i - (i == parts - 1 ? 1 : 0)) * C::kPart; };
+#pragma unroll 1
+        for (int t = warp; t < tasks; t += W) {
+            const int c = t / (D / 32), d = t % (D / 32) * 32 + lane;
+            float top = -INFINITY, l = 0.f, acc = 0.f;
+            constexpr int U = 8;                                // parts whose loads are in flight together
+#pragma unroll 1
+            for (int i0 = 0; i0 < parts; i0 += U) {
+                float R1[U], l1[U], v[U], to = top;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool has = i0 + u < parts;
+                    const float *p = base + at(min(i0 + u, parts - 1));
+                    R1[u] = has ? __ldcg(p + C::kCols * D + c) : -INFINITY;
+                    l1[u] = __ldcg(p + C::kCols * (D + 1) + c);
+                    v[u] = __ldcg(p + c * D + d);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) to = fmaxf(to, R1[u]);
+                const float ref = to == -INFINITY ? 0.f : to, f0 = kv_exp2(top - ref);
+                l *= f0;
+                acc *= f0;
+                top = to;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float f1 = kv_exp2(R1[u] - ref);
+                    l += l1[u] * f1;
+                    acc += v[u] * f1;
+                }
+            }
+            kv_out_row(a, chain.z, chain.w, c, C::kCols, D)[d] = __float2half_rn(l == 0.f ? 0.f : acc / l);
+        }
     }
-    kv_out_row(a, seg.b, seg.hc, c, C::kCols, D)[d] = __float2half_rn(sum == 0.f ? 0.f : acc / sum);
 }
 
 }  // namespace zt

@@ -12,6 +12,7 @@ namespace zt {
 constexpr int kKvTile = 16;               // tokens per tile: one k or m extent of the decode kernel's mma
 constexpr unsigned kErrKvPlace = 1u;      // a page index, position or sequence out of range
 constexpr unsigned kErrKvWait = 2u;       // a bounded wait ran out
+constexpr unsigned kErrKvWork = 4u;       // a workspace that was not zero-filled before its first use
 
 // One kv head's tile: K codes | V codes | K scales | V scales.
 template <int D>

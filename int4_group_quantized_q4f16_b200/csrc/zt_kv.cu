@@ -112,17 +112,20 @@ dim3 row_grid(int rows, int items)
     return dim3((unsigned)rows, (unsigned)std::max(1, std::min(most, 2 * 148 / std::max(1, rows) + 1)));
 }
 
+constexpr size_t kArrivedBytes = 1024;     // counters at the workspace's start
+static_assert(kArrivedBytes >= kKvMaxCtas * sizeof(unsigned), "one counter per CTA");
+
 size_t part_bytes(int head_dim, int cols8)
 {
-    return (size_t)kKvMaxCtas * 2 * cols8 * (head_dim + 2) * sizeof(float);
+    return kArrivedBytes + (size_t)kKvMaxCtas * 2 * cols8 * (head_dim + 2) * sizeof(float);
 }
 
 // Columns (query tokens x grouped heads) go through the matrix instruction eight at a time; from nine
 // on, sixteen share one pass over the cache.
 int column_tiles(int cols) { return cols > 8 ? 2 : 1; }
 
-// Segments of at most this many tokens (as far as the page table reaches), one wave of them: a CTA's 16
-// warps take one each, without a second launch.
+// Segments of at most this many tokens (as far as the page table reaches), one wave of them: a CTA takes one
+// each, and nothing goes through the workspace.
 constexpr int kWholeTokens = 1024;
 
 template <int D, int NT>
@@ -138,12 +141,8 @@ int launch_attention(KvAttnArgs &a, void *stream)
         return ZT_ERR_DEVICE;
     const int longest = a.at.max_pages * a.at.page_size;
     a.whole = segments <= sms && longest <= kWholeTokens * C::kWarps / 16;
-    a.ctas = a.whole ? (int)segments : std::min(sms, kKvMaxCtas);
-    const int rc = launch(kv_attn_kernel<D, NT>, dim3((unsigned)a.ctas), C::kWarps * 32, C::kSmem + index, a, stream);
-    if (rc || a.whole) return rc;
-    if (a.ctas == 1) return ZT_OK;
-    return launch(kv_attn_join_kernel<D, NT>, dim3((unsigned)a.ctas - 1, (unsigned)std::min(C::kCols, a.cols)), 128, index,
-                  a, stream);
+    const int ctas = a.whole ? (int)segments : std::min(sms, kKvMaxCtas);
+    return launch(kv_attn_kernel<D, NT>, dim3((unsigned)ctas), C::kWarps * 32, C::kSmem + index, a, stream);
 }
 
 template <int D>
@@ -336,7 +335,8 @@ int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, int q_he
     a.q = h(q);
     a.out = h(out);
     a.lens = lens;
-    a.part = static_cast<float *>(workspace);
+    a.arrived = static_cast<unsigned int *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kArrivedBytes);
     a.ld_q = ld_q;
     a.ld_out = ld_out;
     a.tokens = tokens;

@@ -507,6 +507,7 @@ class Pass:
 # ----------------------------------------------- paged 4-bit KV cache --
 ZT_Q4_KV_ERR_PLACE = 1
 ZT_Q4_KV_ERR_WAIT = 2
+ZT_Q4_KV_ERR_WORKSPACE = 4
 ZT_Q4_KV_MAX_SEQS = 2048
 
 
@@ -689,7 +690,9 @@ class KvAttention(_Launch):
     """Attention of the last tokens of each sequence over a cache that already holds them: q fp16
     [n_seqs, tokens, q_heads, head_dim] (tokens 1..16, rows may be strided), lens int32 [n_seqs] (cached tokens),
     table int32 [n_seqs, max_pages].  run() returns out, like q and contiguous when not given; a query that sees no
-    token gets zeros.  scale defaults to head_dim ** -0.5.  Calls that may overlap need workspaces of their own."""
+    token gets zeros.  scale defaults to head_dim ** -0.5.  workspace (allocated here when not given): uint8, at least
+    kv_attention_workspace_bytes(...), zero-filled before its first use and left so by every call; calls that may overlap
+    need workspaces of their own."""
 
     def __init__(self, cache: KvCache, q, lens, table, layer: int = 0, out=None, scale=None, workspace=None):
         torch = _torch()
@@ -705,7 +708,7 @@ class KvAttention(_Launch):
             raise ValueError(f"table has {table.shape[0]} rows for {seqs} sequences")
         nbytes = kv_attention_workspace_bytes(cache.kv_heads, heads, dim, tokens)
         if workspace is None:
-            workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+            workspace = torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=dev)
         super().__init__("zt_q4_kv_attention", dev,
                          (ctypes.byref(kv), qp, ld_q, heads, tokens, _ints(lens, dev, "lens", 1, seqs),
                           _ints(table, dev, "table", 2), seqs, int(table.shape[1]),
