@@ -75,7 +75,7 @@ struct KvAttnCfg {
     static constexpr int kSmem = kWarps * (kRing + kPartBytes) + kBars + kFlags;   // + KvIndex, 8 bytes per sequence
 };
 
-constexpr int kKvSegTiles = 2;         // what starting and ending a segment costs, in tiles
+constexpr int kKvSegTiles = 4;         // what starting and ending a segment costs, in tiles
 constexpr int kKvWarpTiles = 1;        // tiles per warp below which fewer CTAs are used
 constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
 constexpr float kKvOff = 9.f, kKvRoom = 15.f, kKvRoomLarge = 2.f;
@@ -266,16 +266,53 @@ __device__ __forceinline__ void kv_zero(const KvAttnArgs &a, int b, int hc, int 
         kv_out_row(a, b, hc, i / D, kcols, D)[i % D] = __float2half_rn(0.f);
 }
 
-// A part of a segment that other CTAs share, left in the workspace: value d of column c.
-template <typename C>
-__device__ __forceinline__ void kv_leave(float *part, int c, int d, float top, float l, float acc, int D)
+__device__ __forceinline__ float kv_lds_f32(uint32_t addr)
 {
-    part[c * D + d] = acc;
-    if (d == 0) {
-        part[C::kCols * D + c] = top;
-        part[C::kCols * (D + 1) + c] = l;
-    }
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
 }
+
+// One column's partial results joined in order by a warp: a lane has values lane, lane + 32, ...
+template <int D>
+struct KvSum {
+    float top = -INFINITY, l = 0.f, acc[D / 32] = {};
+    // four partials (reference, sum of p, values); a missing one has the reference -inf, and its values count nothing
+    __device__ __forceinline__ void add(const float (&R)[4], const float (&l1)[4], const float (&v)[4][D / 32])
+    {
+        const float to = fmaxf(fmaxf(fmaxf(R[0], R[1]), fmaxf(R[2], R[3])), top), ref = to == -INFINITY ? 0.f : to;
+        const float f = kv_exp2(top - ref);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] *= f;
+        top = to;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float w = kv_exp2(R[u] - ref);
+            const bool counts = R[u] != -INFINITY;      // a place without a partial may hold anything
+            l += counts ? l1[u] * w : 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] += counts ? v[u][e] * w : 0.f;
+        }
+    }
+    __device__ __forceinline__ void store(__half *row) const
+    {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) row[32 * e + (threadIdx.x & 31)] = __float2half_rn(acc[e] * inv);
+    }
+    // as a partial of `cols` columns: values, then references, then sums
+    __device__ __forceinline__ void leave(float *part, int c, int cols) const
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) part[c * D + 32 * e + lane] = acc[e];
+        if (lane == 0) {
+            part[cols * D + c] = top;
+            part[cols * (D + 1) + c] = l;
+        }
+    }
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnArgs a)
@@ -759,8 +796,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
 
     // Join the segments that this CTA's warps share.  Each is a chain of warps: it starts where the segment begins
     // (or at the first warp with tiles, for one that began in an earlier CTA) and ends with the warp that wrote its
-    // end (or the last warp with tiles).  All warps see the chains alike and take their columns, 32 values at a
-    // time, in turn; a lane weighs all partials by itself, which is shorter than any exchange.
+    // end (or the last warp with tiles).  All warps see the chains alike and take their columns in turn.
     const int mine = lane < W ? flags[lane] : 0;
     const unsigned some = __ballot_sync(0xffffffffu, mine & 1), opens = __ballot_sync(0xffffffffu, mine & 2),
                    begins = __ballot_sync(0xffffffffu, mine & 4), ends = __ballot_sync(0xffffffffu, mine & 8);
@@ -783,34 +819,29 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
         };
         int b, hc;
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b), "=r"(hc) : "r"(part(w0) + C::kPart * 4));
-        const int tasks = kv_columns(a, hc, C::kCols) * (D / 32);
+        const int tasks = kv_columns(a, hc, C::kCols);
 #pragma unroll 1
         for (; task < tasks; task += W) {
-            const int c = task / (D / 32), d = task % (D / 32) * 32 + lane;
-            float f[W], v[W], top = -INFINITY, l = 0.f, acc = 0.f;
+            KvSum<D> sum;
+#pragma unroll 1
+            for (unsigned rest = in; rest;) {
+                // four partials at a time, loaded without branches
+                float R1[4], l1[4], v[4][D / 32];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                f[w] = -INFINITY;
-                v[w] = 0.f;
-                if ((in >> w) & 1u) {
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[w]) : "r"(part(w) + (C::kCols * D + c) * 4));
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[w]) : "r"(part(w) + (c * D + d) * 4));
+                for (int u = 0; u < 4; ++u) {
+                    const bool has = rest != 0u;
+                    const uint32_t p = part(has ? __ffs(rest) - 1 : w0);
+                    rest &= rest - 1u;
+                    R1[u] = kv_lds_f32(p + (C::kCols * D + task) * 4);
+                    l1[u] = kv_lds_f32(p + (C::kCols * (D + 1) + task) * 4);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) v[u][e] = kv_lds_f32(p + (task * D + 32 * e + lane) * 4);
+                    if (!has) R1[u] = -INFINITY;
                 }
-                top = fmaxf(top, f[w]);
+                sum.add(R1, l1, v);
             }
-            const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                f[w] = kv_exp2(f[w] - ref);
-                acc += v[w] * f[w];
-                v[w] = 0.f;
-                if ((in >> w) & 1u)
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[w]) : "r"(part(w) + (C::kCols * (D + 1) + c) * 4));
-            }
-#pragma unroll
-            for (int w = 0; w < W; ++w) l += v[w] * f[w];
-            if (whole) kv_out_row(a, b, hc, c, C::kCols, D)[d] = __float2half_rn(l == 0.f ? 0.f : acc / l);
-            else kv_leave<C>(a.part + (2ll * blockIdx.x + (ends_here ? 0 : 1)) * C::kPart, c, d, top, l, acc, D);
+            if (whole) sum.store(kv_out_row(a, b, hc, task, C::kCols, D));
+            else sum.leave(a.part + (2ll * blockIdx.x + (ends_here ? 0 : 1)) * C::kPart, task, C::kCols);
         }
         task -= tasks;                            // the next chain's tasks follow on
         if (task < 0) task += W;
@@ -838,40 +869,54 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
     for (int k = 0; k < 2; ++k) {
         if (!flags[k]) continue;
         const int4 chain = chains[k];
-        const int parts = chain.y, tasks = kv_columns(a, chain.w, C::kCols) * (D / 32);
+        const int parts = chain.y, cols = kv_columns(a, chain.w, C::kCols);
         const float *base = a.part + (2ll * chain.x + 1) * C::kPart;      // the last part lies one slot earlier
-        auto at = [&](int i) { return (2 * i - (i == parts - 1 ? 1 : 0)) * C::kPart; };
+        // warp w takes column w % cols, and of its parts every q-th: the W / cols warps of a column halve the
+        // rounds of loads; what each has goes through shared memory (the rings are done with)
+        const int q = max(1, W / cols);
+        float *slots = reinterpret_cast<float *>(rings);
 #pragma unroll 1
-        for (int t = warp; t < tasks; t += W) {
-            const int c = t / (D / 32), d = t % (D / 32) * 32 + lane;
-            float top = -INFINITY, l = 0.f, acc = 0.f;
-            constexpr int U = 8;                                // parts whose loads are in flight together
+        for (int c = warp; c < cols * q; c += W) {
+            KvSum<D> sum;
+            const int col = c % cols;
 #pragma unroll 1
-            for (int i0 = 0; i0 < parts; i0 += U) {
-                float R1[U], l1[U], v[U], to = top;
+            for (int i = c / cols; i < parts; i += 4 * q) {
+                float R1[4], l1[4], v[4][D / 32];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const bool has = i0 + u < parts;
-                    const float *p = base + at(min(i0 + u, parts - 1));
-                    R1[u] = has ? __ldcg(p + C::kCols * D + c) : -INFINITY;
-                    l1[u] = __ldcg(p + C::kCols * (D + 1) + c);
-                    v[u] = __ldcg(p + c * D + d);
+                for (int u = 0; u < 4; ++u) {
+                    const int k = i + u * q;
+                    const float *p = base + (2 * min(k, parts - 1) - (k >= parts - 1 ? 1 : 0)) * C::kPart;
+                    R1[u] = __ldcg(p + C::kCols * D + col);
+                    l1[u] = __ldcg(p + C::kCols * (D + 1) + col);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) v[u][e] = __ldcg(p + col * D + 32 * e + lane);
+                    if (k >= parts) R1[u] = -INFINITY;
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) to = fmaxf(to, R1[u]);
-                const float ref = to == -INFINITY ? 0.f : to, f0 = kv_exp2(top - ref);
-                l *= f0;
-                acc *= f0;
-                top = to;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float f1 = kv_exp2(R1[u] - ref);
-                    l += l1[u] * f1;
-                    acc += v[u] * f1;
-                }
+                sum.add(R1, l1, v);
             }
-            kv_out_row(a, chain.z, chain.w, c, C::kCols, D)[d] = __float2half_rn(l == 0.f ? 0.f : acc / l);
+            if (q == 1) sum.store(kv_out_row(a, chain.z, chain.w, col, C::kCols, D));
+            else sum.leave(slots, c, W);
         }
+        if (q == 1) continue;
+        __syncthreads();
+        if (warp < cols) {
+            KvSum<D> sum;
+#pragma unroll 1
+            for (int i = 0; i < q; i += 4) {
+                float R1[4], l1[4], v[4][D / 32];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int c = warp + min(i + u, q - 1) * cols;
+                    R1[u] = i + u < q ? slots[W * D + c] : -INFINITY;
+                    l1[u] = slots[W * (D + 1) + c];
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) v[u][e] = slots[c * D + 32 * e + lane];
+                }
+                sum.add(R1, l1, v);
+            }
+            sum.store(kv_out_row(a, chain.z, chain.w, warp, C::kCols, D));
+        }
+        __syncthreads();
     }
 }
 
