@@ -15,10 +15,26 @@
 // stands), and p goes back to tensor memory, over S, as the second product's A
 // operand: a thread owns a row, so the softmax needs no exchange between threads.
 //
-// Roles.  Warps 0-3 and 4-7: softmax of tile 0 and of tile 1; warp 8: TMA; warp 9:
-// mma.  While one tile's softmax runs, the other tile's products run.  One commit
-// per S of a tile also covers that tile's previous O += p v (issued before it), so
-// a softmax group that has S may rescale O.
+// Roles.  Warps 0-3 and 4-7: softmax of tile 0 and of tile 1; warp 8: TMA; warps
+// 9 and 10: the products of tile 0 and of tile 1; warp 11: the schedule.  While one tile's softmax runs, the other tile's
+// products run; p is handed over in halves, so that O += p v starts on the first 64
+// keys.  One commit per S of a tile also covers that tile's previous O += p v (issued
+// before it), so a softmax group that has S may rescale O.
+//
+// What bounds it.  A pair of tiles takes 1024 tensor-core cycles per 128 keys (D = 128;
+// 1536 with the shared-memory reads of Q, K and V at 128 bytes a cycle) and 2048 cycles
+// of exponentials at 16 a cycle.  Measured at 8192 tokens, 32 heads of 128: 3700 cycles,
+// of which a softmax group waits 1050 for its products, and takes 550 for the maxima and
+// 1370 for the exponentials.  The groups take turns at the exponentials (without: 548 us,
+// with: 504).  Computing 1/8 .. 3/8 of them by polynomial on the fma units made it slower
+// (565 .. 647 us): the chain of one tile, not the exponentials' rate, sets the pace.
+// 8192 tokens causal: 504-527 us, 1040-1090 TFLOP/s; 784 before the groups took turns,
+// the products had a warp per tile and items were taken in order of their weight.
+//
+// Schedule.  The grid has a CTA per work item (sequence, head, block of queries), the
+// heavy blocks first; a CTA that runs keeps taking items whose CTAs have not been
+// launched (clusterlaunchcontrol), so that loads and the first products of an item
+// overlap the end of the one before, and barriers and tensor memory are set up once.
 //
 // Masked places.  Keys behind a sequence's end (the next sequence's, or whatever
 // follows) are masked in S; their V rows within the last 16-key step are zeroed in
@@ -49,8 +65,9 @@ struct PromptCfg {
     static constexpr int kAtom = 128 * 128;                            // bytes
     static constexpr int kTile = kAtoms * kAtom;                       // 16 or 32 KB
     static constexpr int kStages = kAtoms == 2 ? 5 : 8;
-    static constexpr int kBars = 1 + 2 * kStages + 6;
-    static constexpr int kSmem = 2 * kTile + kStages * kTile + kBars * 8 + 16 + 1024;
+    static constexpr int kBars = 2 * kStages + 2 + 2 + 4 + 2 + 2 + 4 + 1 + 2 + 1;
+    static constexpr int kItems = (kBars * 8 + 15) / 16 * 16;                           // two items of 32 bytes, the scheduler's answer
+    static constexpr int kSmem = 2 * kTile + kStages * kTile + kItems + 64 + 16 + 16 + 1024;
     // kind::f16, D f32, A and B f16; the second product's B (V) is N-major (bit 16)
     static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kAttnKeys >> 3) << 17) | (8u << 24);
     static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
@@ -75,6 +92,22 @@ __device__ __forceinline__ void attn_tma_3d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void attn_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// D (+)= A B: A from shared memory, or from tensor memory; B from shared memory
+__device__ __forceinline__ void attn_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add));
+}
+__device__ __forceinline__ void attn_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add));
 }
 
 // 32 columns of this warp's lanes; attn_ld_wait names the registers before their first use
@@ -120,51 +153,129 @@ __device__ __forceinline__ float attn_exp2(float x)
     return r;
 }
 
+__device__ __forceinline__ bool attn_try(uint32_t bar, uint32_t par)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(par) : "memory");
+    return done != 0u;
+}
+
+// One lane of a converged warp, in a form that lets the compiler keep operands of the tensor-core instructions in
+// uniform registers (a compare with the lane number costs ~200 cycles per instruction: 2.5x the kernel's time).
+__device__ __forceinline__ bool attn_elect()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0u;
+}
+
+// Two fp32 values in a 64-bit register.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 f2_split(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float attn_max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // What a CTA works on: one head's query rows row0 .. of a sequence.
 struct PromptItem {
     int q0, k0, nq, nk, row0, head;
     bool any;
 };
 
-// Item `id` of the list (sequence, head, block of queries from the last to the first): the heavy blocks of
-// a causal prompt start first, and CTAs that run together share a head's keys in L2.  Whole warp.
+// Item `id` of the list.  Up to 32 sequences: by block of queries from the longest sequence's last one down, then
+// sequence, then head: the heavy blocks of causal prompts start first and light ones fill in at the end.  (By sequence,
+// head and block some CTAs had 25 % more tiles than the average at 8192 tokens and 32 heads: 654 us, not 504.)  More
+// sequences, which are short ones as a rule: by sequence, then head, then block from the last down.  Whole warp.
 __device__ __forceinline__ PromptItem prompt_item(const PromptArgs &a, int id, int rows)
 {
     PromptItem it{};
     const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-        const int b = b0 + lane;
-        int q0 = 0, nq = 0;
-        if (b < a.n_seqs) {
-            // offsets out of order or range: the sequence is left out
-            const int q1 = a.cu_q[b + 1];
-            q0 = a.cu_q[b];
-            nq = q0 >= 0 && q1 >= q0 && q1 <= a.total_q ? q1 - q0 : 0;
-        }
-        int mine = (nq + rows - 1) / rows * a.q_heads, upto = mine;
+    auto length = [&](int b, int &q0) {
+        if (b >= a.n_seqs) return 0;
+        // offsets out of order or range: the sequence is left out
+        const int q1 = a.cu_q[b + 1];
+        q0 = a.cu_q[b];
+        return q0 >= 0 && q1 >= q0 && q1 <= a.total_q ? q1 - q0 : 0;
+    };
+    auto scan = [&](int v) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, id < before + upto);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int rel = id - before - __shfl_sync(0xffffffffu, upto - mine, src);
-            it.q0 = __shfl_sync(0xffffffffu, q0, src);
-            it.nq = __shfl_sync(0xffffffffu, nq, src);
-            const int k1 = a.cu_k[b0 + src + 1];
-            it.k0 = a.cu_k[b0 + src];
-            it.nk = it.k0 >= 0 && k1 >= it.k0 && k1 <= a.total_k ? k1 - it.k0 : 0;
-            const int blocks = (it.nq + rows - 1) / rows;
-            it.head = rel / blocks;
-            it.row0 = (blocks - 1 - (rel - it.head * blocks)) * rows;
-            it.any = rel >= 0 && it.head < a.q_heads;       // false only where overlapping sequences overflow the count
-            return it;
+        return v;
+    };
+    int src = -1, first = 0, q0 = 0, nq = 0, rel = id, blocks = 0;
+    if (a.n_seqs <= 32) {
+        nq = length(lane, q0);
+        blocks = (nq + rows - 1) / rows;
+        // the highest level (block index) with at most id items above it
+        int lo = 0, hi = __reduce_max_sync(0xffffffffu, blocks);
+        if (hi == 0) return it;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__reduce_add_sync(0xffffffffu, max(blocks - mid, 0)) * a.q_heads > id) lo = mid;
+            else hi = mid;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        rel = id - __reduce_add_sync(0xffffffffu, max(blocks - lo - 1, 0)) * a.q_heads;
+        const int mine = blocks > lo ? a.q_heads : 0, upto = scan(mine);
+        const unsigned hit = __ballot_sync(0xffffffffu, rel < upto);
+        if (!hit) return it;
+        src = __ffs(hit) - 1;
+        it.head = rel - __shfl_sync(0xffffffffu, upto - mine, src);
+        it.row0 = lo * rows;
+    } else {
+        for (int before = 0; first < a.n_seqs; first += 32) {
+            nq = length(first + lane, q0);
+            blocks = (nq + rows - 1) / rows;
+            const int mine = blocks * a.q_heads, upto = scan(mine);
+            const unsigned hit = __ballot_sync(0xffffffffu, id < before + upto);
+            if (hit) {
+                src = __ffs(hit) - 1;
+                rel = id - before - __shfl_sync(0xffffffffu, upto - mine, src);
+                const int n = __shfl_sync(0xffffffffu, blocks, src);
+                it.head = rel / n;
+                it.row0 = (n - 1 - (rel - it.head * n)) * rows;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (src < 0) return it;
     }
+    it.q0 = __shfl_sync(0xffffffffu, q0, src);
+    it.nq = __shfl_sync(0xffffffffu, nq, src);
+    const int k1 = a.cu_k[first + src + 1];
+    it.k0 = a.cu_k[first + src];
+    it.nk = it.k0 >= 0 && k1 >= it.k0 && k1 <= a.total_k ? k1 - it.k0 : 0;
+    // false only where overlapping sequences overflow the count
+    it.any = it.head >= 0 && it.head < a.q_heads && it.row0 >= 0 && it.row0 < it.nq;
     return it;
 }
 
@@ -179,20 +290,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
     extern __shared__ __align__(128) unsigned char attn_smem[];
     const uint32_t raw = kv_smem(attn_smem);
     const uint32_t q_s = (raw + 1023u) & ~1023u, ring = q_s + 2 * C::kTile;
-    const uint32_t bars = ring + S * C::kTile, slot = bars + C::kBars * 8;
-    const uint32_t q_full = bars;
-    auto full = [&](int s) { return bars + 8u * (1 + s); };
-    auto empty = [&](int s) { return bars + 8u * (1 + S + s); };
-    auto s_full = [&](int t) { return bars + 8u * (1 + 2 * S + t); };
-    auto p_full = [&](int t) { return bars + 8u * (3 + 2 * S + t); };
-    auto o_full = [&](int t) { return bars + 8u * (5 + 2 * S + t); };
+    const uint32_t bars = ring + S * C::kTile, items = bars + C::kItems, answer = items + 64, slot = answer + 16;
+    auto full = [&](int s) { return bars + 8u * s; };                       // K or V tile loaded
+    auto empty = [&](int s) { return bars + 8u * (S + s); };                // and used
+    const uint32_t misc = bars + 16u * S;
+    const uint32_t q_full = misc, q_empty = misc + 8;                       // the item's Q tiles loaded, and used
+    auto s_full = [&](int t) { return misc + 16u + 8u * t; };               // S of tile t there
+    auto p_full = [&](int t, int h) { return misc + 32u + 8u * (2 * t + h); };   // half h of its weights there
+    auto o_full = [&](int t) { return misc + 64u + 8u * t; };               // O of tile t complete
+    auto o_empty = [&](int t) { return misc + 80u + 8u * t; };              // and read
+    auto item_full = [&](int i) { return misc + 96u + 8u * i; };            // item slot i written
+    auto item_empty = [&](int i) { return misc + 112u + 8u * i; };          // and read by its eleven readers
+    const uint32_t answered = misc + 128u, wanted = misc + 152u;            // the scheduler's answer; an item's loads issued
+    auto go = [&](int t) { return misc + 136u + 8u * t; };                  // tile t's turn at the exponentials
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kBars; ++i) {
-            const bool p = i >= 3 + 2 * S && i < 5 + 2 * S;
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * i), "r"(p ? 128 : 1) : "memory");
+        auto init = [&](uint32_t bar, int n) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+        };
+        for (int i = 0; i < S; ++i) {
+            init(full(i), 1);
+            init(empty(i), 2);
         }
+        init(q_full, 1);
+        init(q_empty, 2);
+        for (int t = 0; t < 2; ++t) {
+            init(s_full(t), 1);
+            init(p_full(t, 0), 128);
+            init(p_full(t, 1), 128);
+            init(o_full(t), 1);
+            init(o_empty(t), 128);
+            init(go(t), 128);
+            init(item_full(t), 1);
+            init(item_empty(t), 11);
+        }
+        init(answered, 1);
+        init(wanted, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -201,114 +335,158 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
     }
     kv_pdl_launch();
     kv_pdl_wait();
-    const int rows = a.tiles * kAttnRows;
-    const PromptItem it = prompt_item(a, (int)blockIdx.x, rows);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
 
-    // key tiles of each query tile: those that its last row sees
-    auto seen_by = [&](int row) { return a.causal ? min(max(row + 1 + it.nk - it.nq, 0), it.nk) : it.nk; };
-    int n_t[2];
+    // Every wait is bounded; after one ran out its role gives up, and so do, one after the other, those that wait for it.
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t phase) {          // whole warp
+        // one try without a branch per lane; most waits end there
+        if (__all_sync(0xffffffffu, attn_try(bar, phase & 1u))) return;
+        if (ok && !__all_sync(0xffffffffu, tc_wait(bar, phase & 1u, false))) {
+            if (lane == 0) kv_error(a.err, kErrKvWait);
+            ok = false;
+        }
+    };
+    auto arrive = [&](uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); };
+
+    // item number k of this CTA, from the schedule; false: there is none
+    int q0, k0, nq, nk, row0, head, n_t[2], n;
+    auto take = [&](int k) {
+        wait(item_full(k & 1), (uint32_t)k >> 1);
+        const uint32_t at = items + 32u * (k & 1);
+        int any = 0;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q0), "=r"(k0), "=r"(nq), "=r"(nk) : "r"(at) : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(row0), "=r"(head), "=r"(any), "=r"(n) : "r"(at + 16u)
+                     : "memory");
+        __syncwarp();
+        if (lane == 0) arrive(item_empty(k & 1));
+        // the same in all lanes; a reduction's result is known to be, and stays in uniform registers
+        auto uniform = [](int &v) { v = __reduce_max_sync(0xffffffffu, v); };
+        uniform(q0), uniform(k0), uniform(nq), uniform(nk), uniform(row0), uniform(head), uniform(any);
+        // key tiles of each query tile: those that its last row sees
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = it.row0 + t * kAttnRows, last = min(first + kAttnRows, it.nq) - 1;
-        n_t[t] = it.any && t < a.tiles && last >= first ? (seen_by(last) + kAttnKeys - 1) / kAttnKeys : 0;
-    }
-    const int n = max(n_t[0], n_t[1]);
-    const int kv_head = it.head / a.group;
+        for (int t = 0; t < 2; ++t) {
+            const int first = row0 + t * kAttnRows, last = min(first + kAttnRows, nq) - 1;
+            const int seen = a.causal ? min(max(last + 1 + nk - nq, 0), nk) : nk;
+            n_t[t] = t < a.tiles && last >= first ? (seen + kAttnKeys - 1) / kAttnKeys : 0;
+        }
+        n = max(n_t[0], n_t[1]);
+        return ok && any != 0;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        const int t = warp >> 2, row = it.row0 + t * kAttnRows + (threadIdx.x & 127);
-        const bool valid = it.any && t < a.tiles && row < it.nq;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int t = warp >> 2;
+        auto my_n = [&]() { return t ? n_t[1] : n_t[0]; };
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + 128u * t, o_tm = tmem + lanes + 256u + 128u * t;
-        const int seen = seen_by(row);
-        const int all_seen = seen_by(it.row0 + t * kAttnRows);      // by every row of the tile
         const float sl = a.scale_log2, slack = kAttnSlack / sl;
-        float ref = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < n_t[t] && ok; ++j) {
-            ok = __all_sync(0xffffffffu, tc_wait(s_full(t), (uint32_t)j & 1u, false));
-            if (!ok) {
-                if (lane == 0) kv_error(a.err, kErrKvWait);
-                break;
-            }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            uint32_t r[4][32];
+        uint32_t turn = 0, done = 0, pairs = 0;     // S tiles, O tiles and turns at the exponentials taken so far
+        for (int k = 0; take(k); ++k) {
+            const int mine = my_n();
+            const int row = row0 + t * kAttnRows + (threadIdx.x & 127);
+            auto seen_by = [&](int r) { return a.causal ? min(max(r + 1 + nk - nq, 0), nk) : nk; };
+            const int seen = seen_by(row), all_seen = seen_by(row0 + t * kAttnRows);      // by this row, by every row
+            const int both = min(n_t[0], n_t[1]);
+            float ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < mine && ok; ++j, ++turn) {
+                wait(s_full(t), turn);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                uint32_t r[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) attn_ld32(s_tm + 32 * c, r[c]);
+                for (int c = 0; c < 4; ++c) attn_ld32(s_tm + 32 * c, r[c]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) attn_ld_wait(r[c]);
-            if (j * kAttnKeys + kAttnKeys > all_seen) {
-                const int left = seen - j * kAttnKeys;
+                for (int c = 0; c < 4; ++c) attn_ld_wait(r[c]);
+                if (j * kAttnKeys + kAttnKeys > all_seen) {
+                    const int left = seen - j * kAttnKeys;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i >= left) r[c][i] = 0xFF800000u;
+                }
+                float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * c + i >= left) r[c][i] = 0xFF800000u;
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[c][i]));
-            if (__any_sync(0xffffffffu, mx > ref + slack)) {
-                const float to = fmaxf(ref, mx);
-                const float f = ref == to ? 1.f : attn_exp2((ref - to) * sl);
-                ref = to;
-                l *= f;
-                if (j > 0) {
+                    for (int i = 0; i < 32; i += 2)
+                        mx = attn_max3(mx, __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+                if (__any_sync(0xffffffffu, mx > ref + slack)) {
+                    const float to = fmaxf(ref, mx);
+                    const float f = ref == to ? 1.f : attn_exp2((ref - to) * sl);
+                    ref = to;
+                    l *= f;
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        attn_ld32(o_tm + 32 * c, o);
-                        attn_ld_wait(o);
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            attn_ld32(o_tm + 32 * c, o);
+                            attn_ld_wait(o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        attn_st32(o_tm + 32 * c, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            attn_st32(o_tm + 32 * c, o);
+                        }
                     }
                 }
-            }
-            const float base = ref == -INFINITY ? 0.f : ref * sl;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint32_t *src = i < 16 ? r[c] : r[c + 1];
-                    const int k = 2 * (i & 15);
-                    const float p0 = attn_exp2(fmaf(__uint_as_float(src[k]), sl, -base));
-                    const float p1 = attn_exp2(fmaf(__uint_as_float(src[k + 1]), sl, -base));
-                    sum[2 * (i & 1)] += p0;
-                    sum[2 * (i & 1) + 1] += p1;
-                    p[i] = h2_bits(__floats2half2_rn(p0, p1));
+                const float base = ref == -INFINITY ? 0.f : ref * sl;
+                // The two groups take turns at the exponentials: in step, both would wait for them and then both for
+                // the products.
+                const bool paired = j < both;
+                if (paired) {
+                    if (t == 1 || pairs > 0) wait(go(t), pairs - (t == 0));
+                    ++pairs;
+                    if (!ok) break;
                 }
-                attn_st32(s_tm + 16 * c, p);
+                const uint64_t sl2 = f2_pack(sl, sl), base2 = f2_pack(-base, -base);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const uint32_t *src = i < 16 ? r[2 * h] : r[2 * h + 1];
+                        const int e = 2 * (i & 15);
+                        const uint64_t x = f2_fma(f2_pack(__uint_as_float(src[e]), __uint_as_float(src[e + 1])), sl2, base2);
+                        float2 v = f2_split(x);
+                        v.x = attn_exp2(v.x);
+                        v.y = attn_exp2(v.y);
+                        sum[i & 1] = f2_add(sum[i & 1], f2_pack(v.x, v.y));
+                        p[i] = h2_bits(__floats2half2_rn(v.x, v.y));
+                    }
+                    attn_st32(s_tm + 32 * h, p);
+                    if (h == 1 && paired) arrive(go(1 - t));
+                    attn_st_wait();
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    arrive(p_full(t, h));
+                }
+                const float2 s0 = f2_split(sum[0]), s1 = f2_split(sum[1]);
+                l += (s0.x + s0.y) + (s1.x + s1.y);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            attn_st_wait();
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_full(t)) : "memory");
-        }
-        if (n_t[t] > 0 && ok) {
-            ok = __all_sync(0xffffffffu, tc_wait(o_full(t), 0u, false));
-            if (!ok && lane == 0) kv_error(a.err, kErrKvWait);
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        }
-        if (ok) {
+            if (mine > 0) {
+                wait(o_full(t), done++);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
+            if (!ok) break;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            __half *dst = a.out + (long long)(it.q0 + row) * a.ld_out + it.head * D;
+            __half *dst = a.out + (long long)(q0 + row) * a.ld_out + head * D;
+            const bool valid = t < a.tiles && row < nq;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
-                if (n_t[t] > 0) {
+                if (mine > 0) {
                     attn_ld32(o_tm + 32 * c, o);
                     attn_ld_wait(o);
+                }
+                if (c == D / 32 - 1 && mine > 0) {
+                    // all of O is in registers or on its way out: the next item's products may start
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    arrive(o_empty(t));
                 }
                 if (valid) {
 #pragma unroll
@@ -325,115 +503,202 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             }
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    } else if (warp == 8) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
+    if (warp == 8) {
         // ---------------------------------------------------------------- TMA
-        if (lane == 0 && n > 0) {
-            auto tile = [&](uint32_t dst, const CUtensorMap *map, int head, int token, uint32_t bar) {
-#pragma unroll
-                for (int c = 0; c < C::kAtoms; ++c) attn_tma_3d(dst + c * C::kAtom, map, 64 * c, head, token, bar);
-            };
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(q_full), "r"(a.tiles * C::kTile)
-                         : "memory");
-            for (int t = 0; t < a.tiles; ++t) tile(q_s + t * C::kTile, &map_q, it.head, it.q0 + it.row0 + t * kAttnRows, q_full);
-            int i = 0;
-            for (; i < 2 * n; ++i) {
-                const int s = i % S;
-                if (i >= S && !tc_wait(empty(s), (uint32_t)(i / S - 1) & 1u, false)) {
-                    kv_error(a.err, kErrKvWait);
-                    break;
-                }
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full(s)), "r"(C::kTile) : "memory");
-                tile(ring + s * C::kTile, (i & 1) ? &map_v : &map_k, kv_head, it.k0 + (i >> 1) * kAttnKeys, full(s));
+        int i = 0, qs = 0;                                        // tiles and items with queries loaded so far
+        bool q_open = false;
+        for (int k = 0; take(k); ++k) {
+            if (n == 0) {
+                if (lane == 0) arrive(wanted);
+                continue;
             }
-            // every load has landed before the CTA ends (all of them have been used, unless a wait ran out)
-            tc_wait(q_full, 0u, false);
-            for (int k = max(0, i - S); k < i; ++k)
-                if (!tc_wait(full(k % S), (uint32_t)(k / S) & 1u, false)) break;
+            const int kv_head = head / a.group;
+            auto tile = [&](uint32_t dst, const CUtensorMap *map, int h, int token, uint32_t bar) {
+#pragma unroll
+                for (int c = 0; c < C::kAtoms; ++c) attn_tma_3d(dst + c * C::kAtom, map, 64 * c, h, token, bar);
+            };
+            auto expect = [&](uint32_t bar, int bytes) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+            };
+            if (qs > 0) wait(q_empty, (uint32_t)(qs - 1));
+            if (!ok) break;
+            if (lane == 0) {
+                expect(q_full, a.tiles * C::kTile);
+                for (int t = 0; t < a.tiles; ++t) tile(q_s + t * C::kTile, &map_q, head, q0 + row0 + t * kAttnRows, q_full);
+            }
+            ++qs;
+            q_open = true;
+            for (int j = 0; j < 2 * n; ++j, ++i) {
+                const int s = i % S;
+                if (i >= S) wait(empty(s), (uint32_t)(i / S - 1));
+                if (!ok) break;
+                if (lane == 0) {
+                    expect(full(s), C::kTile);
+                    tile(ring + s * C::kTile, (j & 1) ? &map_v : &map_k, kv_head, k0 + (j >> 1) * kAttnKeys, full(s));
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) arrive(wanted);
+        }
+        // every load has landed before the CTA ends (all of them have been used, unless a wait ran out)
+        if (lane == 0) {
+            if (q_open) tc_wait(q_full, (uint32_t)(qs - 1) & 1u, false);
+            for (int j = max(0, i - S); j < i; ++j)
+                if (!tc_wait(full(j % S), (uint32_t)(j / S) & 1u, false)) break;
         }
         __syncwarp();
-    } else if (warp == 9 && n > 0) {
+    } else if (warp == 9 || warp == 10) {
         // ---------------------------------------------------------------- mma
-        bool ok = true;
-        auto wait = [&](uint32_t bar, int par) {
-            if (ok && !__all_sync(0xffffffffu, tc_wait(bar, (uint32_t)par & 1u, false))) {
-                if (lane == 0) kv_error(a.err, kErrKvWait);
-                ok = false;
-            }
+        // One warp per query tile: what one of them spends between products is hidden by the other's.
+        const int t = warp - 9;
+        const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + 128u * t, q_t = q_s + t * C::kTile;
+        auto sync_wait = [&](uint32_t bar, uint32_t phase) {
+            wait(bar, phase);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         };
-        auto scores = [&](int t, int j) {
-            const int i = 2 * j;
-            const uint64_t dq = tc_desc_sw128(q_s + t * C::kTile), dk = tc_desc_sw128(ring + (i % S) * C::kTile);
-            if (lane == 0) {
+        auto scores = [&](int i) {                                // S with the keys of ring tile i
+            const uint64_t dq = tc_desc_sw128(q_t), dk = tc_desc_sw128(ring + (i % S) * C::kTile);
+            if (attn_elect()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t at = (uint64_t)((k / 4) * (C::kAtom >> 4) + (k % 4) * 2);
-                    asm volatile(
-                        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + 128u * t),
-                        "l"(dq + at), "l"(dk + at), "r"(C::kIdescS), "r"(k ? 1u : 0u));
+                    attn_mma_ss(s_tm, dq + at, dk + at, C::kIdescS, k > 0);
                 }
                 attn_commit(s_full(t));
             }
         };
-        auto values = [&](int t, int j, int steps) {
-            const int i = 2 * j + 1;
-            const uint64_t dv = attn_desc_v(ring + (i % S) * C::kTile, C::kAtom);
-            if (lane == 0)
+        auto values = [&](int j, int i, int h, int steps) {       // O += half h of p v, `steps` 16-key steps
+            const uint64_t dv = attn_desc_v(ring + (i % S) * C::kTile + h * 8192, C::kAtom);
+            const uint32_t p = s_tm + 32u * h;
+            if (attn_elect()) {
+                if (steps >= 4) {
 #pragma unroll
-                for (int k = 0; k < kAttnKeys / 16; ++k)
-                    if (k < steps)
-                        asm volatile(
-                            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + 256u + 128u * t),
-                            "r"(tmem + 128u * t + 8u * k), "l"(dv + (uint64_t)(k * (2048 >> 4))), "r"(C::kIdescO),
-                            "r"((j | k) ? 1u : 0u));
-        };
-        wait(q_full, 0);
-        wait(full(0), 0);
-        if (ok) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (n_t[t] > 0) scores(t, 0);
-            if (lane == 0 && S < 2 * n) attn_commit(empty(0));
-        }
-        for (int j = 0; j < n && ok; ++j) {
-            const int iv = 2 * j + 1, ik = 2 * j + 2;
-            wait(full(iv % S), iv / S);
-            const int keys = min(kAttnKeys, it.nk - j * kAttnKeys), steps = (keys + 15) / 16;
-            if (keys < 16 * steps && ok) {
-                // rows behind the end within the last step: zero, whatever follows the sequence
-                for (int c = lane; c < (16 * steps - keys) * C::kAtoms * 8; c += 32) {
-                    const int row = keys + c / (C::kAtoms * 8), in = c % (C::kAtoms * 8);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + (iv % S) * C::kTile +
-                                                                                 (in / 8) * C::kAtom + row * 128 + (in % 8) * 16),
-                                 "r"(0u) : "memory");
+                    for (int k = 0; k < 4; ++k)
+                        attn_mma_ts(o_tm, p + 8u * k, dv + (uint64_t)(k * 128), C::kIdescO, j > 0 || h > 0 || k > 0);
+                } else {
+                    for (int k = 0; k < steps; ++k)
+                        attn_mma_ts(o_tm, p + 8u * k, dv + (uint64_t)(k * 128), C::kIdescO, j > 0 || h > 0 || k > 0);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
             }
-            if (ik < 2 * n) wait(full(ik % S), ik / S);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (j >= n_t[t]) continue;
-                wait(p_full(t), j);
+        };
+        // this warp is done with what `bar` guards: when the products issued so far are, or at once.  Both warps say
+        // so for every tile and item, after its load: neither can be a phase ahead of the other.
+        auto release = [&](uint32_t bar, bool used) {
+            if (attn_elect()) {
+                if (used) attn_commit(bar);
+                else arrive(bar);
+            }
+        };
+        int base = 0, qs = 0;                                     // ring tiles and Q tiles of the items before
+        uint32_t turn = 0, outs = 0;                              // S tiles and O tiles of this query tile so far
+        for (int k = 0; take(k); ++k) {
+            if (n == 0) continue;
+            const int mine = t ? n_t[1] : n_t[0];
+            sync_wait(q_full, (uint32_t)qs);
+            sync_wait(full(base % S), (uint32_t)(base / S));
+            if (!ok) break;
+            if (mine > 0) scores(base);
+            release(empty(base % S), mine > 0);
+            if (mine < 2) release(q_empty, mine > 0);
+            for (int j = 0; j < n && ok; ++j) {
+                const int iv = base + 2 * j + 1, ik = iv + 1;
+                sync_wait(full(iv % S), (uint32_t)(iv / S));
+                const int keys = min(kAttnKeys, nk - j * kAttnKeys), steps = (keys + 15) / 16;
+                if (keys < 16 * steps && ok) {
+                    // rows behind the end within the last step: zero, whatever follows the sequence (both warps write
+                    // the same zeros)
+                    for (int c = lane; c < (16 * steps - keys) * C::kAtoms * 8; c += 32) {
+                        const int row = keys + c / (C::kAtoms * 8), in = c % (C::kAtoms * 8);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + (iv % S) * C::kTile + (in / 8) * C::kAtom + row * 128 + (in % 8) * 16),
+                                     "r"(0u) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (j + 1 < n) sync_wait(full(ik % S), (uint32_t)(ik / S));
+                if (j < mine) {
+                    if (j == 0 && outs > 0) sync_wait(o_empty(t), outs - 1);
+                    sync_wait(p_full(t, 0), turn);
+                    if (!ok) break;
+                    values(j, iv, 0, steps);
+                    sync_wait(p_full(t, 1), turn);
+                    if (!ok) break;
+                    values(j, iv, 1, steps - 4);
+                    ++turn;
+                    if (j + 1 < mine) scores(ik);
+                    else {
+                        release(o_full(t), true);
+                        ++outs;
+                    }
+                }
                 if (!ok) break;
-                values(t, j, steps);
-                if (j + 1 < n_t[t]) scores(t, j + 1);
-                else if (lane == 0) attn_commit(o_full(t));
+                release(empty(iv % S), j < mine);
+                if (j + 1 < n) release(empty(ik % S), j + 1 < mine);
+                if (j + 2 == mine) release(q_empty, true);        // the last scores have read Q
             }
-            if (ok && lane == 0) {
-                // only for stages that are loaded again: no arrival is left behind when the CTA ends
-                if (iv + S < 2 * n) attn_commit(empty(iv % S));
-                if (ik + S < 2 * n) attn_commit(empty(ik % S));
-            }
+            if (!ok) break;
+            base += 2 * n;
+            ++qs;
         }
-        if (!ok && lane == 0) {
-            // what was issued ends before tensor memory is freed
-            attn_commit(o_full(0));
-            tc_wait(o_full(0), 0u, false);
+        // all commits have arrived before shared and tensor memory are given back
+        if (ok) {
+            if (qs > 0) wait(q_empty, (uint32_t)(qs - 1));
+            for (int i = max(0, base - S); i < base; ++i) wait(empty(i % S), (uint32_t)(i / S));
+        } else if (attn_elect()) {
+            attn_commit(o_empty(t));                              // what was issued ends first: any free barrier will do
+            tc_wait(o_empty(t), 0u, false);
         }
         __syncwarp();
+    } else if (warp == 11) {
+        // ----------------------------------------------------------- schedule
+        int id = blockIdx.x;
+        for (int k = 0;; ++k) {
+            const PromptItem it = id >= 0 ? prompt_item(a, id, a.tiles * kAttnRows) : PromptItem{};
+            // a CTA without an item: the list is shorter than the grid, and so are all that follow
+            if (k >= 2) wait(item_empty(k & 1), (uint32_t)(k >> 1) - 1u);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t at = items + 32u * (k & 1);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(it.q0), "r"(it.k0), "r"(it.nq), "r"(it.nk)
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16u), "r"(it.row0), "r"(it.head),
+                             "r"(it.any ? 1 : 0), "r"(0) : "memory");
+                arrive(item_full(k & 1));
+            }
+            __syncwarp();
+            if (!it.any) break;
+            // the next item is taken when this one's loads have been issued: earlier, it would wait here while other
+            // CTAs run out of work
+            wait(wanted, (uint32_t)k);
+            if (!ok) break;
+            if (lane == 0) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(answered) : "memory");
+                asm volatile(
+                    "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                        answer),
+                    "r"(answered) : "memory");
+            }
+            wait(answered, (uint32_t)k);
+            if (!ok) break;
+            uint32_t got, x;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+                "ld.shared.b128 r, [%2];\n\t"
+                "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+                : "=r"(got), "=r"(x)
+                : "r"(answer)
+                : "memory");
+            // the answer has been read before the next one may be written over it
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            id = got ? (int)x : -1;
+        }
     }
     __syncthreads();
     if (warp == 8) {
