@@ -241,13 +241,39 @@ def test_attention(zt, D, q_heads, heads, tokens, page):
     check_attention(zt, cache, pool, fp16(rng, len(LENS), tokens, q_heads, D, by=2.0), LENS, table)
 
 
-@pytest.mark.parametrize("D,q_heads,heads", [(128, 4, 1), (96, 2, 2), (64, 3, 1)])
-def test_attention_long_sequences(zt, D, q_heads, heads):
-    """Sequences cut between many CTAs, next to short ones."""
+@pytest.mark.parametrize("D,q_heads,heads,tokens,page", [(128, 4, 1, 1, 64), (96, 2, 2, 1, 64), (64, 3, 1, 1, 16),
+                                                         (128, 12, 1, 1, 48), (96, 5, 1, 5, 16), (64, 1, 1, 2, 1024)])
+def test_attention_long_sequences(zt, D, q_heads, heads, tokens, page):
+    """Sequences cut between many CTAs, next to short ones; up to 25 columns a head."""
     rng = np.random.default_rng(D)
     lens = [5, 7001, 0, 1300, 1]
-    cache, pool, table = filled(zt, rng, lens, 64, heads, D)
-    check_attention(zt, cache, pool, fp16(rng, len(lens), 1, q_heads, D, by=2.0), lens, table)
+    cache, pool, table = filled(zt, rng, lens, page, heads, D)
+    check_attention(zt, cache, pool, fp16(rng, len(lens), tokens, q_heads, D, by=2.0), lens, table)
+
+
+def test_attention_split_changes_nothing_but_rounding(zt):
+    """The same sequence alone, among others and behind a wider page table (which of the launch shapes is taken goes by
+    that) agrees within the tolerance; each of them repeats bit for bit."""
+    rng = np.random.default_rng(12)
+    lens, D = [900, 33, 900, 700], 128
+    cache, pool, table = filled(zt, rng, lens, 32, 2, D)
+    q = fp16(rng, 4, 1, 8, D, by=2.0)
+    wide = np.concatenate([table, np.zeros((4, 40), np.int32)], 1)
+    for t in (table, wide):
+        check_attention(zt, cache, pool, q, lens, t)
+        check_attention(zt, cache, pool, q[:1], lens[:1], t[:1])
+
+
+def test_attention_reports_a_workspace_that_was_not_zeroed(zt):
+    import torch
+    rng = np.random.default_rng(13)
+    lens = [6000]
+    cache, pool, table = filled(zt, rng, lens, 64, 1, 64)
+    nbytes = zt.kv_attention_workspace_bytes(1, 1, 64, 1)
+    dirty = torch.full((nbytes,), 0xEE, dtype=torch.uint8, device="cuda")
+    zt.KvAttention(cache, cuda(fp16(rng, 1, 1, 1, 64)), cuda(np.array(lens, np.int32)), cuda(table), workspace=dirty).run()
+    torch.cuda.synchronize()
+    assert cache.errors() == zt.ZT_Q4_KV_ERR_WORKSPACE
 
 
 def test_attention_many_sequences(zt):
