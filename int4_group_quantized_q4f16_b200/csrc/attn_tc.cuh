@@ -411,12 +411,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                         for (int i = 0; i < 32; ++i)
                             if (32 * c + i >= left) r[c][i] = 0xFF800000u;
                 }
-                float mx = -INFINITY;
+                float m4[4];                             // four chains: one would be 64 dependent steps
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    m4[c] = __uint_as_float(r[c][0]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        mx = attn_max3(mx, __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+                    for (int i = 1; i < 31; i += 2)
+                        m4[c] = attn_max3(m4[c], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+                    m4[c] = fmaxf(m4[c], __uint_as_float(r[c][31]));
+                }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (__any_sync(0xffffffffu, mx > ref + slack)) {
                     const float to = fmaxf(ref, mx);
                     const float f = ref == to ? 1.f : attn_exp2((ref - to) * sl);

@@ -555,25 +555,19 @@ class _Launch:
     current stream (or `stream`).  The tensors are kept alive; their contents are read at run()."""
 
     def __init__(self, name, device, args, keep, result):
-        self._fn, self._name, self._args, self._keep, self._result = getattr(lib, name), name, args, keep, result
-        self._device = device
-
-    def _launch(self, stream):
         torch = _torch()
-        if stream is None:
-            # the raw handle: building torch's Stream object takes longer than a launch
-            stream = torch._C._cuda_getCurrentRawStream(self._device.index)
-        else:
-            stream = _stream_handle(stream)
-        _check(self._fn(*self._args, stream), self._name)
+        self._fn, self._name, self._args, self._keep, self._result = getattr(lib, name), name, args, keep, result
+        self._device, self._index = device, device.index
+        # the raw handle: building torch's Stream object takes longer than a launch
+        self._current, self._raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
 
     def run(self, stream=None):
-        torch = _torch()
-        if torch.cuda.current_device() == self._device.index:
-            self._launch(stream)
-        else:
-            with torch.cuda.device(self._device):
-                self._launch(stream)
+        if self._current() != self._index:
+            with _torch().cuda.device(self._device):
+                return self.run(stream)
+        rc = self._fn(*self._args, self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+        if rc != ZT_OK:
+            raise ZtError(rc, self._name)
         return self._result
 
 
