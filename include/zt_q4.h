@@ -480,8 +480,8 @@ ZT_API int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int
  * q 16-byte, out 2-byte aligned), q_heads * head_dim values each.  lens: int32
  * [n_seqs] (DEVICE): tokens of each sequence in the cache.  A query that sees no
  * token gives zeros.  n_seqs <= ZT_Q4_KV_MAX_SEQS; q_heads a multiple of kv_heads.
- * Scores, softmax statistics and sums are fp32; the weights are rounded to fp16
- * before and after they are multiplied by V's scales.
+ * Scores, softmax statistics and sums are fp32; the products of the weights and V's
+ * scales are rounded to fp16.
  * workspace: DEVICE, 16-byte aligned, zt_q4_kv_attention_workspace_bytes() bytes
  * (a function of these sizes alone).  Unlike the other workspaces of this library
  * it must be ZERO-FILLED before its first use: it holds counters that every call
@@ -511,7 +511,12 @@ ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, i
  * 0 .. 2^24 (pointers to tensors without rows are not looked at).  Rows of out that no sequence covers are left as they were.
  * A sequence whose offsets decrease or leave total_q (total_k) is treated as one
  * without queries (keys).  Scores, softmax statistics and sums are fp32; the
- * weights are rounded to fp16 for the second product.  err (DEVICE, 4-byte
+ * weights are rounded to fp16 for the second product.  Keys that a query does not
+ * see have weight zero in it, so a NaN or an infinity in v of a later token of the
+ * same sequence can reach earlier queries of that sequence (0 * NaN); other
+ * sequences' rows, and rows of k and v that no sequence covers, never do.  The call
+ * takes further work as its CTAs finish, so which CTA computes what varies; results
+ * do not.  err (DEVICE, 4-byte
  * aligned, or NULL): bit 1 is OR-ed in if a bounded wait (2 s) ran out.  One launch.
  */
 ZT_API int zt_q4_prompt_attention(const uint16_t *q, int ld_q, const uint16_t *k, int ld_k, const uint16_t *v,

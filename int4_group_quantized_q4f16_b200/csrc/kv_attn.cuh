@@ -27,7 +27,9 @@
 // 15.  That keeps p * vs in the upper range of fp16: with scales below 2 (values
 // below 14) p * vs stays under 2^16, and a weight of 2^-24 of the largest one still
 // has 2 bits.  A tile with a larger scale sets the two to 0 and 2 (p <= 4, p * vs <=
-// 4 * 65504 / 7).  p is rounded to fp16, p * vs once more; sums of p and O are fp32.
+// 4 * 65504 / 7).  p goes through the transpose as two fp16 parts, so that p * vs is
+// rounded once (with p rounded first, the error of a long sequence's output was 1.5
+// times that of its rounding to fp16 alone, not 1.3); sums of p and O are fp32.
 //
 // Work split.  The (sequence, kv head) segments are laid end to end in tiles, each
 // with two more that stand for its own cost, and cut into equal runs, one per CTA,
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                     }
                 }
         }
-        uint32_t pt[NT][2][2];
+        uint32_t pt[NT][2][2], pl[NT][2][2];      // the weights as B fragments: rounded, and what the rounding left
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // a column that has seen nothing yet keeps R = -inf: its weights are 2^-inf = 0
@@ -701,8 +703,12 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                 const float p2 = kv_exp2(fmaf(P[nt][u][2], sl, -r0)), p3 = kv_exp2(fmaf(P[nt][u][3], sl, -r1));
                 L[nt][0] += p0 + p2;
                 L[nt][1] += p1 + p3;
-                pt[nt][u][0] = kv_transpose(h2_bits(__floats2half2_rn(p0, p1)));
-                pt[nt][u][1] = kv_transpose(h2_bits(__floats2half2_rn(p2, p3)));
+                const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
+                const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+                pt[nt][u][0] = kv_transpose(h2_bits(h01));
+                pt[nt][u][1] = kv_transpose(h2_bits(h23));
+                pl[nt][u][0] = kv_transpose(h2_bits(__floats2half2_rn(p0 - f01.x, p1 - f01.y)));
+                pl[nt][u][1] = kv_transpose(h2_bits(__floats2half2_rn(p2 - f23.x, p3 - f23.y)));
             }
         }
 #pragma unroll
@@ -721,8 +727,9 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t b0 = h2_bits(__hmul2(bits_h2(pt[nt][u][0]), bits_h2(vs[u][2 * g])));
-                    uint32_t b1 = h2_bits(__hmul2(bits_h2(pt[nt][u][1]), bits_h2(vs[u][2 * g + 1])));
+                    const __half2 s0 = bits_h2(vs[u][2 * g]), s1 = bits_h2(vs[u][2 * g + 1]);
+                    uint32_t b0 = h2_bits(__hfma2(bits_h2(pt[nt][u][0]), s0, __hmul2(bits_h2(pl[nt][u][0]), s0)));
+                    uint32_t b1 = h2_bits(__hfma2(bits_h2(pt[nt][u][1]), s1, __hmul2(bits_h2(pl[nt][u][1]), s1)));
                     if (mend) {
                         b0 = kv_hide(b0, pt[nt][u][0]);
                         b1 = kv_hide(b1, pt[nt][u][1]);
