@@ -439,9 +439,9 @@ typedef struct zt_q4_kv_rope {
     float theta;              /* > 0 */
     const uint16_t *q;        /* fp16 [n][ld_q], q_heads * head_dim values per row, or NULL */
     int ld_q, q_heads;
-    uint16_t *q_out;          /* fp16 [n][ld_q_out], with q; q itself is not allowed */
+    uint16_t *q_out;          /* fp16 [n][ld_q_out], with q; may not overlap it */
     int ld_q_out;
-    uint16_t *k_out;          /* fp16 [n][ld_k_out] receives the rotated k, or NULL */
+    uint16_t *k_out;          /* fp16 [n][ld_k_out] receives the rotated k (may not overlap k), or NULL */
     int ld_k_out;
 } zt_q4_kv_rope;
 
@@ -479,9 +479,10 @@ ZT_API int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int
  * q and out: fp16, row b * tokens + i of ld_q / ld_out elements (multiples of 8;
  * q 16-byte, out 2-byte aligned), q_heads * head_dim values each.  lens: int32
  * [n_seqs] (DEVICE): tokens of each sequence in the cache.  A query that sees no
- * token gives zeros.  n_seqs <= ZT_Q4_KV_MAX_SEQS; q_heads a multiple of kv_heads.
+ * token gives zeros.  n_seqs <= ZT_Q4_KV_MAX_SEQS; q_heads a multiple of kv_heads;
+ * scale between 2^-64 and 2^64.
  * Scores, softmax statistics and sums are fp32; the products of the weights and V's
- * scales are rounded to fp16.
+ * scales are rounded to fp16.  out may not overlap q or the pool.
  * workspace: DEVICE, 16-byte aligned, zt_q4_kv_attention_workspace_bytes() bytes
  * (a function of these sizes alone).  Unlike the other workspaces of this library
  * it must be ZERO-FILLED before its first use: it holds counters that every call
@@ -508,7 +509,9 @@ ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, i
  * Rows of q, k, v and out hold q_heads or kv_heads heads of head_dim (64, 96 or
  * 128) side by side, ld elements apart (multiples of 8; 16-byte aligned bases);
  * q_heads a multiple of kv_heads; n_seqs <= ZT_Q4_KV_MAX_SEQS; total_q, total_k
- * 0 .. 2^24 (pointers to tensors without rows are not looked at).  Rows of out that no sequence covers are left as they were.
+ * 0 .. 2^24 (pointers to tensors without rows are not looked at); out overlaps none of
+ * the inputs; scale between 2^-64
+ * and 2^64.  Rows of out that no sequence covers are left as they were.
  * A sequence whose offsets decrease or leave total_q (total_k) is treated as one
  * without queries (keys).  Scores, softmax statistics and sums are fp32; the
  * weights are rounded to fp16 for the second product.  Keys that a query does not

@@ -32,7 +32,7 @@
 // times that of its rounding to fp16 alone, not 1.3); sums of p and O are fp32.
 //
 // Work split.  The (sequence, kv head) segments are laid end to end in tiles, each
-// with two more that stand for its own cost, and cut into equal runs, one per CTA,
+// with four more that stand for its own cost, and cut into equal runs, one per CTA,
 // then one per warp: ragged batches and single long sequences balance alike.  Each
 // warp streams its run through a private ring of bulk copies (a tile is K and V),
 // two tiles at a time.  Where every segment is short and there are few of them, a
@@ -40,6 +40,19 @@
 // memory; of the CTAs that share a segment each leaves its part in the workspace and
 // counts itself, and the one that counts last joins them.  Both joins go in the
 // order of the tokens: results do not depend on timing.
+//
+// What bounds it.  One token of 131071 cached ones, 8 kv heads of 128, 4 query heads each
+// (151 MB of cache): 46.5 us, 3.2 TB/s; the copies alone, without the products, 25.7 us.  The
+// main loop is bound by issue slots: a pair of tiles takes a warp about 600 instructions, most
+// of them unpacking codes for the two products.  Joining the warps takes 2 us of it and joining
+// the CTAs 5 us, most of that latency.  61 sequences of up to 6001 tokens (174 MB): 57 us; 7
+// sequences of up to 3999 tokens, 32 kv heads of 96, 4 query tokens (27 MB): 21 us; one sequence
+// of 517 tokens (1.8 MB): 8.0 us, of which streaming takes 4.1, the products 2.7 and the join 1.1.
+// Warps: 16 with two pairs of tiles in flight each; 8 with four pairs took 54.0, 67.2 and 22.4 us
+// on the first three.  Columns: eight at a time.  Sixteen that share a pass over the tiles (8 warps,
+// for the registers) took 30.1 us where two passes of eight take 24.0 (4 sequences of 20000 tokens,
+// 12 columns per kv head; 16 columns: 32.6 and 25.3), and were faster only where the cache is larger
+// than L2: 131071 tokens of 8 heads, 16 columns, 79.3 and 80.7; 32 sequences of 8000, 57.4 and 64.6.
 #pragma once
 
 #include "kv_common.cuh"
@@ -56,18 +69,18 @@ struct KvAttnArgs {
     long long ld_q, ld_out;    // elements between query tokens
     int tokens;                // query tokens per sequence
     int q_heads, group;        // group = q_heads / kv_heads
-    int cols, blocks;          // columns of a kv head (tokens * group), and blocks of 8 NT of them
+    int cols, blocks;          // columns of a kv head (tokens * group), and blocks of 8 of them
     int whole;                 // 1: a CTA takes one whole segment
     float scale_log2;          // softmax scale * log2(e)
 };
 
-template <int D, int NT>
+template <int D>
 struct KvAttnCfg {
     using T = KvTile<D>;
-    static constexpr int kWarps = NT == 1 ? 16 : 8;
+    static constexpr int kWarps = 16;
     static constexpr int kPairs = D == 64 ? 4 : 2;      // ring stages of two tiles
     static constexpr int kStage = 2 * T::kBytes;
-    static constexpr int kCols = 8 * NT;
+    static constexpr int kCols = 8;
     static constexpr int kPart = kCols * (D + 2);                      // floats: O, then R and the sum of p per column
     static constexpr int kRing = kPairs * kStage;                      // per warp; holds the last partial at the end
     static constexpr int kPartBytes = (kPart * 4 + 8 + 15) / 16 * 16;         // and the segment, within a CTA
@@ -77,8 +90,9 @@ struct KvAttnCfg {
     static constexpr int kSmem = kWarps * (kRing + kPartBytes) + kBars + kFlags;   // + KvIndex, 8 bytes per sequence
 };
 
-constexpr int kKvSegTiles = 4;         // what starting and ending a segment costs, in tiles
-constexpr int kKvWarpTiles = 1;        // tiles per warp below which fewer CTAs are used
+// What starting and ending a segment costs, in tiles.  131071 tokens of 8 heads, 61 ragged sequences, 7 with 4
+// query tokens: with 1 48.6, 63.7 and 22.5 us, 2 48.5, 56.9 and 20.8, 4 46.5, 57.0 and 20.9, 8 46.7, 57.3 and 20.7.
+constexpr int kKvSegTiles = 4;
 constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
 constexpr float kKvOff = 9.f, kKvRoom = 15.f, kKvRoomLarge = 2.f;
 
@@ -93,10 +107,10 @@ struct KvRuns {
     }
 };
 
-// Number of CTAs that share `total` tiles.
+// Number of CTAs that share `total` tiles: a tile per warp at least.
 __device__ __forceinline__ int kv_ctas(int total, int ctas, int warps)
 {
-    return max(1, min(ctas, (total + warps * kKvWarpTiles - 1) / (warps * kKvWarpTiles)));
+    return max(1, min(ctas, (total + warps - 1) / warps));
 }
 
 // Cached tokens of sequence b: its length, at most what its row of the page table holds.
@@ -316,10 +330,10 @@ struct KvSum {
     }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnArgs a)
+template <int D>
+__global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnArgs a)
 {
-    using C = KvAttnCfg<D, NT>;
+    using C = KvAttnCfg<D>;
     using T = KvTile<D>;
     constexpr int G = T::kG, W = C::kWarps, S = C::kPairs;
     extern __shared__ __align__(128) unsigned char kv_smem_raw[];
@@ -505,9 +519,9 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
         for (int s = 0; s < C::kPairs && to_copy > 0; ++s) issue(s);
     }
 
-    float O[NT][D / 16][4], R[NT][2], L[NT][2], most[NT][2];
-    uint32_t qf[NT][G][4], xq[NT];
-    int seen[NT][2];                 // tokens that columns 2j and 2j + 1 see
+    float O[D / 16][4], R[2], L[2], most[2];
+    uint32_t qf[G][4], xq;
+    int seen[2];                 // tokens that columns 2j and 2j + 1 see
     float off = kKvOff;
     const float sl = a.scale_log2 * 0x1p24f, inv_sl = 1.f / sl;
     bool fresh = true, dead = false;
@@ -520,46 +534,43 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
             seg_tile0 = seg.tile;
             off = kKvOff;
             const int h = seg.hc / a.blocks, c0 = (seg.hc - h * a.blocks) * C::kCols;
+            const int col = c0 + r;
+            const bool has = col < a.cols;
+            const int i = has ? col / a.group : 0, qh = h * a.group + (has ? col - i * a.group : 0);
+            const __half *q = a.q + ((long long)seg.b * a.tokens + i) * a.ld_q + qh * D + 8 * j;
+            __half xlo = __float2half_rn(0.f), xhi = xlo;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int col = c0 + nt * 8 + r;
-                const bool has = col < a.cols;
-                const int i = has ? col / a.group : 0, qh = h * a.group + (has ? col - i * a.group : 0);
-                const __half *q = a.q + ((long long)seg.b * a.tokens + i) * a.ld_q + qh * D + 8 * j;
-                __half xlo = __float2half_rn(0.f), xhi = xlo;
+            for (int g = 0; g < G; ++g) {
+                const uint4 w = has ? *reinterpret_cast<const uint4 *>(q + 32 * g) : make_uint4(0, 0, 0, 0);
+                const float2 f0 = __half22float2(bits_h2(w.x)), f1 = __half22float2(bits_h2(w.y)),
+                             f2 = __half22float2(bits_h2(w.z)), f3 = __half22float2(bits_h2(w.w));
+                float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                // lane j of a quad keeps the two groups of its k slots: groups 0..3 rounded to fp16 in
+                // slots 0..3, what the rounding left in slots 4..7 (2^-8 of them, so that none overflows)
+                sum *= -7.f * 0x1p-8f;
+                const __half high = __float2half_rn(sum);
+                const __half part = j < 2 ? high : __float2half_rn(sum - __half2float(high));
+                if (g / 2 == (j & 1)) (g & 1 ? xhi : xlo) = part;
+                // step 0 of a group meets codes 0, 4 | 2, 6 of the lane's word, step 1 codes 1, 5 | 3, 7,
+                // which come with a factor 16
+                const __half2 six = __float2half2_rn(0.0625f);
+                qf[g][0] = __byte_perm(w.x, w.z, 0x5410);
+                qf[g][1] = __byte_perm(w.y, w.w, 0x5410);
+                qf[g][2] = h2_bits(__hmul2(bits_h2(__byte_perm(w.x, w.z, 0x7632)), six));
+                qf[g][3] = h2_bits(__hmul2(bits_h2(__byte_perm(w.y, w.w, 0x7632)), six));
+            }
+            xq = h2_bits(__halves2half2(xlo, xhi));
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint4 w = has ? *reinterpret_cast<const uint4 *>(q + 32 * g) : make_uint4(0, 0, 0, 0);
-                    const float2 f0 = __half22float2(bits_h2(w.x)), f1 = __half22float2(bits_h2(w.y)),
-                                 f2 = __half22float2(bits_h2(w.z)), f3 = __half22float2(bits_h2(w.w));
-                    float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    // lane j of a quad keeps the two groups of its k slots: groups 0..3 rounded to fp16 in
-                    // slots 0..3, what the rounding left in slots 4..7 (2^-8 of them, so that none overflows)
-                    sum *= -7.f * 0x1p-8f;
-                    const __half high = __float2half_rn(sum);
-                    const __half part = j < 2 ? high : __float2half_rn(sum - __half2float(high));
-                    if (g / 2 == (j & 1)) (g & 1 ? xhi : xlo) = part;
-                    // step 0 of a group meets codes 0, 4 | 2, 6 of the lane's word, step 1 codes 1, 5 | 3, 7,
-                    // which come with a factor 16
-                    const __half2 six = __float2half2_rn(0.0625f);
-                    qf[nt][g][0] = __byte_perm(w.x, w.z, 0x5410);
-                    qf[nt][g][1] = __byte_perm(w.y, w.w, 0x5410);
-                    qf[nt][g][2] = h2_bits(__hmul2(bits_h2(__byte_perm(w.x, w.z, 0x7632)), six));
-                    qf[nt][g][3] = h2_bits(__hmul2(bits_h2(__byte_perm(w.y, w.w, 0x7632)), six));
-                }
-                xq[nt] = h2_bits(__halves2half2(xlo, xhi));
+            for (int m = 0; m < D / 16; ++m)
 #pragma unroll
-                for (int m = 0; m < D / 16; ++m)
+                for (int e = 0; e < 4; ++e) O[m][e] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) O[nt][m][e] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    R[nt][e] = most[nt][e] = -INFINITY;
-                    L[nt][e] = 0.f;
-                    seen[nt][e] = seg.len - a.tokens + 1 + (c0 + nt * 8 + 2 * j + e) / a.group;
-                }
+            for (int e = 0; e < 2; ++e) {
+                R[e] = most[e] = -INFINITY;
+                L[e] = 0.f;
+                seen[e] = seg.len - a.tokens + 1 + (c0 + 2 * j + e) / a.group;
             }
         }
         // Two tiles at a time, for independent work between the waits and one look at the maxima; a last
@@ -577,7 +588,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
         const bool drop0 = dead || ((bad >> (2 * s)) & 1u), drop1 = dead || step < 2 || ((bad >> (2 * s)) & 2u);
         const uint32_t stage = ring + s * C::kStage;
         const uint32_t tile[2] = {stage, stage + T::kBytes};
-        float P[NT][2][4];
+        float P[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t wa[G], wb[G], ks[G], kz[2];
@@ -597,27 +608,21 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
             for (int g = 0; g < G; ++g) {
                 const float2 sc = __half22float2(bits_h2(ks[g]));
                 const uint32_t ha = wa[g] >> 8, hb = wb[g] >> 8;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float d[4];
-                    float (&p)[4] = P[nt][u];
-                    kv_mma(d, wa[g] & 0x000F000Fu, wb[g] & 0x000F000Fu, ha & 0x000F000Fu, hb & 0x000F000Fu, qf[nt][g][0],
-                           qf[nt][g][1], 0.f, 0.f, 0.f, 0.f);
-                    kv_mma(d, wa[g] & 0x00F000F0u, wb[g] & 0x00F000F0u, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[nt][g][2],
-                           qf[nt][g][3], d[0], d[1], d[2], d[3]);
-                    p[0] = g ? fmaf(sc.x, d[0], p[0]) : sc.x * d[0];
-                    p[1] = g ? fmaf(sc.x, d[1], p[1]) : sc.x * d[1];
-                    p[2] = g ? fmaf(sc.y, d[2], p[2]) : sc.y * d[2];
-                    p[3] = g ? fmaf(sc.y, d[3], p[3]) : sc.y * d[3];
-                }
+                float d[4];
+                float (&p)[4] = P[u];
+                kv_mma(d, wa[g] & 0x000F000Fu, wb[g] & 0x000F000Fu, ha & 0x000F000Fu, hb & 0x000F000Fu, qf[g][0],
+                       qf[g][1], 0.f, 0.f, 0.f, 0.f);
+                kv_mma(d, wa[g] & 0x00F000F0u, wb[g] & 0x00F000F0u, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[g][2],
+                       qf[g][3], d[0], d[1], d[2], d[3]);
+                p[0] = g ? fmaf(sc.x, d[0], p[0]) : sc.x * d[0];
+                p[1] = g ? fmaf(sc.x, d[1], p[1]) : sc.x * d[1];
+                p[2] = g ? fmaf(sc.y, d[2], p[2]) : sc.y * d[2];
+                p[3] = g ? fmaf(sc.y, d[3], p[3]) : sc.y * d[3];
             }
+            float z[4];
+            kv_mma(z, za, zb, 0u, 0u, xq, 0u, 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float z[4];
-                kv_mma(z, za, zb, 0u, 0u, xq[nt], 0u, 0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) P[nt][u][e] = fmaf(z[e], 0x1p-16f, P[nt][u][e]);
-            }
+            for (int e = 0; e < 4; ++e) P[u][e] = fmaf(z[e], 0x1p-16f, P[u][e]);
         }
         // the V scales of this lane's tokens 2j, 2j + 1 and 2j + 8, 2j + 9
         uint32_t vs[2][2 * G];
@@ -640,10 +645,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                 const bool drop = u ? drop1 : drop0;
                 const int tu = t0 + u * kKvTile;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (drop || tu + r + 8 * (e >> 1) >= seen[nt][e & 1]) P[nt][u][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e)
+                    if (drop || tu + r + 8 * (e >> 1) >= seen[e & 1]) P[u][e] = -INFINITY;
                 // places behind the sequence's end may hold anything
 #pragma unroll
                 for (int g = 0; g < G; ++g)
@@ -666,50 +669,43 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
         const bool large = (any & 0x40004000u) != 0u;                // a scale of 2 or more
         bool lift = large && off > 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                lift |= fmaxf(fmaxf(P[nt][0][e], P[nt][0][e + 2]), fmaxf(P[nt][1][e], P[nt][1][e + 2])) > most[nt][e];
+        for (int e = 0; e < 2; ++e)
+            lift |= fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2])) > most[e];
         if (__any_sync(0xffffffffu, lift)) {
             const float before = off;
             if (__any_sync(0xffffffffu, large)) off = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2])) * sl;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(fmaxf(P[nt][0][e], P[nt][0][e + 2]), fmaxf(P[nt][1][e], P[nt][1][e + 2])) * sl;
+                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float ref = fmaxf(mx, R[e] + before) - off;
+                const float f = R[e] == ref ? 1.f : kv_exp2(R[e] - ref);
+                R[e] = ref;
+                most[e] = (ref + (off > 0.f ? kKvRoom : kKvRoomLarge)) * inv_sl;
+                L[e] *= f;
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const float ref = fmaxf(mx, R[nt][e] + before) - off;
-                    const float f = R[nt][e] == ref ? 1.f : kv_exp2(R[nt][e] - ref);
-                    R[nt][e] = ref;
-                    most[nt][e] = (ref + (off > 0.f ? kKvRoom : kKvRoomLarge)) * inv_sl;
-                    L[nt][e] *= f;
-#pragma unroll
-                    for (int m = 0; m < D / 16; ++m) {
-                        O[nt][m][e] *= f;
-                        O[nt][m][e + 2] *= f;
-                    }
+                for (int m = 0; m < D / 16; ++m) {
+                    O[m][e] *= f;
+                    O[m][e + 2] *= f;
                 }
-        }
-        uint32_t pt[NT][2][2], pl[NT][2][2];      // the weights as B fragments: rounded, and what the rounding left
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // a column that has seen nothing yet keeps R = -inf: its weights are 2^-inf = 0
-            const float r0 = R[nt][0] == -INFINITY ? 0.f : R[nt][0], r1 = R[nt][1] == -INFINITY ? 0.f : R[nt][1];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float p0 = kv_exp2(fmaf(P[nt][u][0], sl, -r0)), p1 = kv_exp2(fmaf(P[nt][u][1], sl, -r1));
-                const float p2 = kv_exp2(fmaf(P[nt][u][2], sl, -r0)), p3 = kv_exp2(fmaf(P[nt][u][3], sl, -r1));
-                L[nt][0] += p0 + p2;
-                L[nt][1] += p1 + p3;
-                const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
-                const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
-                pt[nt][u][0] = kv_transpose(h2_bits(h01));
-                pt[nt][u][1] = kv_transpose(h2_bits(h23));
-                pl[nt][u][0] = kv_transpose(h2_bits(__floats2half2_rn(p0 - f01.x, p1 - f01.y)));
-                pl[nt][u][1] = kv_transpose(h2_bits(__floats2half2_rn(p2 - f23.x, p3 - f23.y)));
             }
+        }
+        uint32_t pt[2][2], pl[2][2];      // the weights as B fragments: rounded, and what the rounding left
+        // a column that has seen nothing yet keeps R = -inf: its weights are 2^-inf = 0
+        const float r0 = R[0] == -INFINITY ? 0.f : R[0], r1 = R[1] == -INFINITY ? 0.f : R[1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float p0 = kv_exp2(fmaf(P[u][0], sl, -r0)), p1 = kv_exp2(fmaf(P[u][1], sl, -r1));
+            const float p2 = kv_exp2(fmaf(P[u][2], sl, -r0)), p3 = kv_exp2(fmaf(P[u][3], sl, -r1));
+            L[0] += p0 + p2;
+            L[1] += p1 + p3;
+            const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
+            const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+            pt[u][0] = kv_transpose(h2_bits(h01));
+            pt[u][1] = kv_transpose(h2_bits(h23));
+            pl[u][0] = kv_transpose(h2_bits(__floats2half2_rn(p0 - f01.x, p1 - f01.y)));
+            pl[u][1] = kv_transpose(h2_bits(__floats2half2_rn(p2 - f23.x, p3 - f23.y)));
         }
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -725,20 +721,17 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
                     va[i][2] = kv_value(hi & 0x000F000Fu, kKvLow);
                     va[i][3] = kv_value(hi & 0x00F000F0u, kKvHigh);
                 }
+                const __half2 s0 = bits_h2(vs[u][2 * g]), s1 = bits_h2(vs[u][2 * g + 1]);
+                uint32_t b0 = h2_bits(__hfma2(bits_h2(pt[u][0]), s0, __hmul2(bits_h2(pl[u][0]), s0)));
+                uint32_t b1 = h2_bits(__hfma2(bits_h2(pt[u][1]), s1, __hmul2(bits_h2(pl[u][1]), s1)));
+                if (mend) {
+                    b0 = kv_hide(b0, pt[u][0]);
+                    b1 = kv_hide(b1, pt[u][1]);
+                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const __half2 s0 = bits_h2(vs[u][2 * g]), s1 = bits_h2(vs[u][2 * g + 1]);
-                    uint32_t b0 = h2_bits(__hfma2(bits_h2(pt[nt][u][0]), s0, __hmul2(bits_h2(pl[nt][u][0]), s0)));
-                    uint32_t b1 = h2_bits(__hfma2(bits_h2(pt[nt][u][1]), s1, __hmul2(bits_h2(pl[nt][u][1]), s1)));
-                    if (mend) {
-                        b0 = kv_hide(b0, pt[nt][u][0]);
-                        b1 = kv_hide(b1, pt[nt][u][1]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float (&o)[4] = O[nt][2 * g + i];
-                        kv_mma(o, va[i][0], va[i][1], va[i][2], va[i][3], b0, b1, o[0], o[1], o[2], o[3]);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    float (&o)[4] = O[2 * g + i];
+                    kv_mma(o, va[i][0], va[i][1], va[i][2], va[i][3], b0, b1, o[0], o[1], o[2], o[3]);
                 }
             }
         __syncwarp();                                                     // all lanes have read the stage
@@ -763,36 +756,34 @@ __global__ void __launch_bounds__(KvAttnCfg<D, NT>::kWarps * 32, 1) kv_attn_kern
             }
             __syncwarp();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 2; ++e) {
+                float l = L[e];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float l = L[nt][e];
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const int c = 2 * j + e;
+                if (c >= kv_columns(a, seg.hc, C::kCols)) continue;
+                if (whole) {
+                    __half *row = kv_out_row(a, seg.b, seg.hc, c, C::kCols, D);
+                    const float inv = l == 0.f ? 0.f : 0x1p10f / l;
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    const int c = nt * 8 + 2 * j + e;
-                    if (c >= kv_columns(a, seg.hc, C::kCols)) continue;
-                    if (whole) {
-                        __half *row = kv_out_row(a, seg.b, seg.hc, c, C::kCols, D);
-                        const float inv = l == 0.f ? 0.f : 0x1p10f / l;
+                    for (int m = 0; m < D / 16; ++m) {
+                        row[16 * m + r] = __float2half_rn(O[m][e] * inv);
+                        row[16 * m + 8 + r] = __float2half_rn(O[m][e + 2] * inv);
+                    }
+                } else {
 #pragma unroll
-                        for (int m = 0; m < D / 16; ++m) {
-                            row[16 * m + r] = __float2half_rn(O[nt][m][e] * inv);
-                            row[16 * m + 8 + r] = __float2half_rn(O[nt][m][e + 2] * inv);
-                        }
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < D / 16; ++m) {
-                            dst[c * D + 16 * m + r] = O[nt][m][e] * 0x1p10f;
-                            dst[c * D + 16 * m + 8 + r] = O[nt][m][e + 2] * 0x1p10f;
-                        }
-                        if (r == 0) {
-                            dst[C::kCols * D + c] = R[nt][e];
-                            dst[C::kCols * (D + 1) + c] = l;
-                            reinterpret_cast<int *>(dst)[C::kPart] = seg.b;
-                            reinterpret_cast<int *>(dst)[C::kPart + 1] = seg.hc;
-                        }
+                    for (int m = 0; m < D / 16; ++m) {
+                        dst[c * D + 16 * m + r] = O[m][e] * 0x1p10f;
+                        dst[c * D + 16 * m + 8 + r] = O[m][e + 2] * 0x1p10f;
+                    }
+                    if (r == 0) {
+                        dst[C::kCols * D + c] = R[e];
+                        dst[C::kCols * (D + 1) + c] = l;
+                        reinterpret_cast<int *>(dst)[C::kPart] = seg.b;
+                        reinterpret_cast<int *>(dst)[C::kPart + 1] = seg.hc;
                     }
                 }
+            }
             fresh = true;
         }
         seg.tile += step;

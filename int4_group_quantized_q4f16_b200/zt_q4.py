@@ -703,11 +703,14 @@ class KvAttention(_Launch):
         nbytes = kv_attention_workspace_bytes(cache.kv_heads, heads, dim, tokens)
         if workspace is None:
             workspace = torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        _on(workspace, dev, torch.uint8, "workspace", 1)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         super().__init__("zt_q4_kv_attention", dev,
                          (ctypes.byref(kv), qp, ld_q, heads, tokens, _ints(lens, dev, "lens", 1, seqs),
                           _ints(table, dev, "table", 2), seqs, int(table.shape[1]),
                           float(dim ** -0.5 if scale is None else scale), op, ld_out, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size()),
+                          workspace.numel()),
                          (cache, q, lens, table, out, workspace, kv), out)
 
     @staticmethod

@@ -402,3 +402,17 @@ def test_graph_stream_and_workspace(zt):
         replayed = first._result.clone()
         assert torch.equal(first.run(stream=side), replayed) and not torch.equal(replayed, want[0])
     torch.cuda.synchronize()
+
+
+def test_attention_refuses_other_workspaces(zt):
+    import torch
+    cache = zt.KvCache.empty(1, 4, 16, 2, 64)
+    q = torch.zeros((1, 1, 2, 64), dtype=torch.float16, device="cuda")
+    lens, table = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((1,), (1, 2)))
+    n = zt.kv_attention_workspace_bytes(2, 2, 64, 1)
+    for bad in (torch.zeros(n, dtype=torch.uint8), torch.zeros(n, dtype=torch.int8, device="cuda"),
+                torch.zeros((2, n), dtype=torch.uint8, device="cuda"), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            zt.KvAttention(cache, q, lens, table, workspace=bad)
+    with pytest.raises(zt.ZtError):
+        zt.KvAttention(cache, q, lens, table, workspace=torch.zeros(n - 1, dtype=torch.uint8, device="cuda")).run()

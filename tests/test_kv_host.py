@@ -105,7 +105,7 @@ def test_copy_refusals(zt):
 
 def test_attention_refusals(zt):
     ws = zt.kv_attention_workspace_bytes(2, 8, 64, 1)
-    assert ws > 0 and zt.kv_attention_workspace_bytes(2, 8, 64, 4) > ws
+    assert ws > 0 and zt.kv_attention_workspace_bytes(2, 8, 128, 4) > ws
     for bad in ((0, 8, 64, 1), (2, 7, 64, 1), (2, 1, 64, 1), (2, 8, 32, 1), (2, 8, 64, 0), (2, 8, 64, 17)):
         assert zt.kv_attention_workspace_bytes(*bad) == 0
 
@@ -121,6 +121,7 @@ def test_attention_refusals(zt):
                       (dict(table=None), "INVALID_ARG"), (dict(seqs=0), "INVALID_ARG"), (dict(seqs=2049), "INVALID_ARG"),
                       (dict(max_pages=0), "INVALID_ARG"), (dict(scale=0.0), "INVALID_ARG"), (dict(scale=-1.0), "INVALID_ARG"),
                       (dict(scale=float("nan")), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG"),
+                      (dict(scale=2.0**65), "INVALID_ARG"), (dict(scale=2.0**-65), "INVALID_ARG"),
                       (dict(out=None), "INVALID_ARG"), (dict(out=FAKE + 1), "MISALIGNED"), (dict(ld=511), "INVALID_ARG"),
                       (dict(work=None), "INVALID_ARG"), (dict(work=FAKE + 8), "MISALIGNED"), (dict(nbytes=ws - 1), "WORKSPACE"),
                       (dict(seqs=2048, max_pages=2**19), "UNSUPPORTED")):
@@ -141,7 +142,8 @@ def test_prompt_refusals(zt):
                       (dict(seqs=2049), "INVALID_ARG"), (dict(total_q=-1), "INVALID_ARG"), (dict(total_k=2**25), "INVALID_ARG"),
                       (dict(heads=7), "INVALID_ARG"), (dict(kv_heads=0), "INVALID_ARG"), (dict(heads=1), "INVALID_ARG"),
                       (dict(dim=80), "UNSUPPORTED"), (dict(dim=256), "UNSUPPORTED"), (dict(causal=2), "INVALID_ARG"),
-                      (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG")):
+                      (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG"),
+                      (dict(scale=2.0**65), "INVALID_ARG"), (dict(scale=2.0**-65), "INVALID_ARG")):
         assert call(**bad) == status(zt, name), bad
     assert call(total_q=0, q=None, out=None) == zt.ZT_OK
 
