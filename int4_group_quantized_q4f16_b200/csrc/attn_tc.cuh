@@ -2,11 +2,13 @@
 // (include/zt_q4.h: zt_q4_prompt_attention).
 //
 // Mathematics.  For a query row, over the keys that it sees, in tiles of 128:
-//   S = q k^T,  p = 2^(scale log2(e) (S - m)),  O += p v,  l += sum p
+//   S = q k^T,  p = 2^(scale log2(e) (S - m) + 7),  O += p v,  l += sum p
 // and the result is O / l.  m is a reference, at least the largest score so far
-// minus 8 / (scale log2(e)): while scores stay below m by that margin (p <= 2^8),
-// neither O nor l is rescaled.  p is rounded to fp16 for the second product;
-// scores, m, l and O are fp32.
+// minus 8 / (scale log2(e)): while no score passes m by more (p <= 2^15), neither O
+// nor l is rescaled.  p is rounded to fp16 for the second product, and the 7 keeps it
+// in the upper range: of many small weights beside a large one those down to 2^-21 of
+// it are rounded like normal numbers, and 2^-31 is not zero yet (2^-14 and 2^-24
+// without).  Scores, m, l and O are fp32.
 //
 // Layout.  A CTA takes two tiles of 128 queries of one head (one where that leaves
 // SMs idle) and walks the keys.  Both products are tcgen05.mma (M = 128, kind::f16):
@@ -47,7 +49,8 @@ namespace zt {
 
 constexpr int kAttnRows = 128, kAttnKeys = 128;
 constexpr int kAttnThreads = 384;
-constexpr float kAttnSlack = 8.f;      // log2 of the largest weight before a rescale
+constexpr float kAttnSlack = 8.f;      // scores above the reference before a rescale, in powers of two
+constexpr float kAttnLift = 7.f;       // log2 of a weight at the reference
 
 struct PromptArgs {
     __half *out;
@@ -168,32 +171,6 @@ __device__ __forceinline__ bool attn_elect()
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e != 0u;
-}
-
-// Two fp32 values in a 64-bit register.
-__device__ __forceinline__ uint64_t f2_pack(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 f2_split(uint64_t v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 __device__ __forceinline__ float attn_max3(float a, float b, float c)
@@ -438,7 +415,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                         }
                     }
                 }
-                const float base = ref == -INFINITY ? 0.f : ref * sl;
+                const float base = ref == -INFINITY ? 0.f : ref * sl - kAttnLift;
                 // The two groups take turns at the exponentials: in step, both would wait for them and then both for
                 // the products.
                 const bool paired = j < both;

@@ -191,3 +191,16 @@ def test_prompt_graph_and_stream(zt):
         replayed = plan._result.clone()
         assert torch.equal(plan.run(stream=side), replayed) and not torch.equal(replayed, want)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("at", [0, 70000, 2**17])
+def test_prompt_sink(zt, at):
+    """2^17 keys with 2^-26 of the weight of one more, whose value is zero: together 2^-9 of the output.  A weight is 2^-19 as
+    the kernel holds it, an fp16 subnormal with a step of 2^-24: off by 2^-6 of itself at most.  The other errors (O summed in
+    fp32 in 2^13 steps of 2^-24, the score's 2^-19, the output's rounding 2^-11) stay below 2^-9."""
+    n, D = 2**17, 64
+    q, k, v = np.ones((1, 1, D), np.float16), np.zeros((n + 1, 1, D), np.float16), np.ones((n + 1, 1, D), np.float16)
+    k[at], v[at] = 1.0, 0.0
+    got = run(zt, q, k, v, [1], [n + 1], causal=False, scale=26 * np.log(2) / D)
+    want = 2.0**-9 / (1 + 2.0**-9)
+    assert (np.abs(got.astype(np.float64) - want) <= (2.0**-6 + 2.0**-9) * want).all()
