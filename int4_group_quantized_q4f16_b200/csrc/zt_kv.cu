@@ -107,13 +107,25 @@ int launch(void (*fn)(Args), dim3 grid, int threads, size_t smem, const Args &ar
     return e == cudaSuccess ? ZT_OK : device_error(e, ZT_ERR_LAUNCH);
 }
 
-// Few rows leave most SMs idle: a row's values are spread over CTAs until the grid covers the device about
-// twice.  Appending one row with rotation (3 x 32 heads of 96): 5.6 us spread, 9.0 in one CTA; 2384 rows, appended
-// and read back: 66.1 us in a CTA each, 84.7 spread (the rotation's angles are computed in every CTA of a row).
-dim3 row_grid(int rows, int items)
+// CTAs per row or window: few leave most SMs idle, so the items of each are spread until the grid covers the device
+// about twice.  (Rows are not spread further: each CTA of a row computes its angles.)
+int spread(int parts, int items, int threads)
 {
-    const int most = std::max(1, (items + 255) / 256);
-    return dim3((unsigned)rows, (unsigned)std::max(1, std::min(most, 2 * 148 / std::max(1, rows) + 1)));
+    const int most = std::max(1, (items + threads - 1) / threads);
+    return std::max(1, std::min(most, 2 * 148 / std::max(1, parts) + 1));
+}
+
+// Grid of an append or a gather: CTAs by row, then by window of rows.
+template <typename Args>
+int launch_rows(void (*fn)(Args), Args &a, int threads, int row_items, int group_items, void *stream)
+{
+    const int windows = (a.rows + kKvWindow - 1) / kKvWindow;
+    a.row_ctas = spread(a.rows, row_items, threads);
+    // Windows have no angles: up to eight times as many CTAs.  Appending and reading back as in kv_cache.cuh, with 256
+    // threads: 37.1 and 22.7 us, with these 38.6 and 17.9; a CTA per window 66.4 (windows last) and 26.8.
+    a.v_ctas = spread(windows / 8, group_items * 4 * std::min(a.rows, 4), threads);
+    const int64_t grid = (int64_t)a.rows * a.row_ctas + (int64_t)windows * a.v_ctas;
+    return launch(fn, dim3((unsigned)grid), threads, 0, a, stream);
 }
 
 constexpr size_t kArrivedBytes = 1024;     // counters at the workspace's start
@@ -253,10 +265,11 @@ int zt_q4_kv_append(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, const uint16_
         a.q_heads = rope->q ? rope->q_heads : 0;
         for (int i = 0; i < kv->head_dim / 2; ++i) a.freq[i] = std::pow((double)rope->theta, -2.0 * i / kv->head_dim);
     }
-    const dim3 grid = row_grid(rows->n, (2 * kv->kv_heads + a.q_heads) * kv->head_dim / 8);
-    if (kv->head_dim == 64) return launch(kv_append_kernel<64>, grid, 256, 0, a, stream);
-    if (kv->head_dim == 96) return launch(kv_append_kernel<96>, grid, 256, 0, a, stream);
-    return launch(kv_append_kernel<128>, grid, 256, 0, a, stream);
+    a.rows = rows->n;
+    const int row_items = (kv->kv_heads + a.q_heads) * kv->head_dim / 8, groups = kv->kv_heads * kv->head_dim / 32;
+    if (kv->head_dim == 64) return launch_rows(kv_append_kernel<64>, a, kAppendThreads, row_items, groups, stream);
+    if (kv->head_dim == 96) return launch_rows(kv_append_kernel<96>, a, kAppendThreads, row_items, groups, stream);
+    return launch_rows(kv_append_kernel<128>, a, kAppendThreads, row_items, groups, stream);
 }
 
 int zt_q4_kv_gather(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, uint16_t *k, int ld_k, uint16_t *v, int ld_v,
@@ -276,10 +289,11 @@ int zt_q4_kv_gather(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, uint16_t *k, 
     a.v = h(v);
     a.ld_k = ld_k;
     a.ld_v = ld_v;
-    const dim3 grid = row_grid(rows->n, 2 * kv->kv_heads * kv->head_dim / 8);
-    if (kv->head_dim == 64) return launch(kv_gather_kernel<64>, grid, 256, 0, a, stream);
-    if (kv->head_dim == 96) return launch(kv_gather_kernel<96>, grid, 256, 0, a, stream);
-    return launch(kv_gather_kernel<128>, grid, 256, 0, a, stream);
+    a.rows = rows->n;
+    const int row_items = kv->kv_heads * kv->head_dim / 8, groups = kv->kv_heads * kv->head_dim / 32;
+    if (kv->head_dim == 64) return launch_rows(kv_gather_kernel<64>, a, kGatherThreads, row_items, groups, stream);
+    if (kv->head_dim == 96) return launch_rows(kv_gather_kernel<96>, a, kGatherThreads, row_items, groups, stream);
+    return launch_rows(kv_gather_kernel<128>, a, kGatherThreads, row_items, groups, stream);
 }
 
 int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int32_t *dst, int n, int layers,
