@@ -134,6 +134,40 @@ def test_append_is_bit_exact_and_gathers_back(zt, D, heads, page):
         assert np.array_equal(k[i], wk, equal_nan=True) and np.array_equal(v[i], wv, equal_nan=True), i
 
 
+@pytest.mark.parametrize("D,heads,page,where", [(64, 2, 16, "in order"), (96, 3, 32, "in order"), (128, 1, 64, "in order"),
+                                                 (96, 2, 16, "backwards"), (96, 2, 16, "two by two"), (64, 1, 48, "gaps")])
+def test_append_runs(zt, D, heads, page, where):
+    """Rows as prompts and steps bring them: runs of consecutive positions that start and end anywhere in a tile and in a
+    window of rows, runs that touch, padding inside them, rows of a tile in other orders."""
+    rng = np.random.default_rng(D + heads + len(where))
+    spans = [(0, 40), (3, 4), (12, 45), (5, 5), (31, 33), (9, 25), (15, 17), (2, 50), (0, 16), (7, 8), (16, 79)]
+    places = [(b, p) for b, (lo, hi) in enumerate(spans) for p in range(lo, hi)]
+    if where == "backwards":
+        places = places[::-1]
+    elif where == "two by two":
+        places = [x for i in range(0, len(places), 4) for x in places[i + 2:i + 4] + places[i:i + 2]]
+    elif where == "gaps":
+        places = [(b, p if rng.random() < 0.8 else -1) for b, p in places]
+    table, n = tables(rng, [hi for _, hi in spans], page)
+    raw = rng.integers(0, 256, (n, zt.kv_page_bytes(page, heads, D)), dtype=np.uint8)
+    want, cache, rows = ref.Pool(raw.copy(), page, heads, D), zt.KvCache(cuda(raw), page, heads, D), len(places)
+    x = fp16(rng, rows, 2 * heads, D)
+    seq, pos = (np.array(c, np.int32) for c in zip(*places))
+    dev, (sd, pd, td) = cuda(x), (cuda(a) for a in (seq, pos, table))
+    zt.KvAppend(cache, dev[:, :heads], dev[:, heads:], sd, pd, td).run()
+    for i, (b, p) in enumerate(places):
+        if p >= 0:
+            want.write(table[b, p // page], p % page, x[i, :heads], x[i, heads:])
+    same_bytes(cache, want)
+    k, v = (t.cpu().numpy() for t in zt.KvGather(cache, sd, pd, td, k=cuda(np.full((rows, heads, D), 9, np.float16)),
+                                                 v=cuda(np.full((rows, heads, D), 9, np.float16))).run())
+    assert cache.errors() == 0
+    for i, (b, p) in enumerate(places):
+        wk, wv = (ref.dequantize(*ref.quantize(y)).astype(np.float16) if p >= 0 else np.full((heads, D), 9, np.float16)
+                  for y in (x[i, :heads], x[i, heads:]))
+        assert np.array_equal(k[i], wk) and np.array_equal(v[i], wv), (i, b, p)
+
+
 @pytest.mark.parametrize("D,heads,q_heads", [(64, 2, 6), (96, 32, 32), (128, 8, 32)])
 def test_append_rotates(zt, D, heads, q_heads):
     rng = np.random.default_rng(D)
