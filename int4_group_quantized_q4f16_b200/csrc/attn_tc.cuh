@@ -38,6 +38,10 @@
 // launched (clusterlaunchcontrol), so that loads and the first products of an item
 // overlap the end of the one before, and barriers and tensor memory are set up once.
 //
+// Few query tiles on long keys (a chunk behind a prefix): the CTAs of a cluster share an item's keys, leave O, the
+// references and the sums in shared memory, and each joins a share of the columns, reading the others' through the
+// cluster, in the order of the keys.  No workspace, one launch.
+//
 // Masked places.  Keys behind a sequence's end (the next sequence's, or whatever
 // follows) are masked in S; their V rows within the last 16-key step are zeroed in
 // shared memory and later steps skipped, so what they hold does not matter.
@@ -58,6 +62,7 @@ struct PromptArgs {
     const int32_t *cu_q, *cu_k;        // [n_seqs + 1]
     int n_seqs, total_q, total_k, q_heads, group, causal;
     int tiles;                         // query tiles per CTA: 1 or 2
+    int splits;                        // CTAs (a cluster) that share an item's keys; more than 1 with one query tile only
     float scale_log2;
     unsigned int *err;
 };
@@ -256,7 +261,65 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptArgs &a, int id, i
     return it;
 }
 
-template <int D>
+// The cluster's parts of an item, in shared memory: O as [D][128 rows], the rows' references and sums behind it.  A cluster
+// barrier separates writing, joining and the end; every thread comes to it, whatever became of its role.
+__device__ __forceinline__ void attn_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float attn_peer(uint32_t saddr, int rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .b32 at;\n\tmapa.shared::cluster.u32 at, %1, %2;\n\tld.shared::cluster.f32 %0, [at];\n\t}"
+                 : "=f"(v) : "r"(saddr), "r"(rank));
+    return v;
+}
+
+constexpr int kAttnSplits = 8;         // CTAs of a cluster that share an item's keys, at most
+
+// One row's result from N parts, in their order: CTA `rank` of the cluster writes its share of the columns, with 32 reads
+// under way at a time.
+template <int D, int N>
+__device__ __forceinline__ void attn_join(uint32_t part, int row, int rank, float sl, __half *dst)
+{
+    constexpr int kShare = D / N, kStep = 32 / N;
+    static_assert(kShare % kStep == 0 && kStep % 4 == 0, "whole steps, of 8 bytes of the result");
+    const uint32_t refs = part + D * kAttnRows * 4 + row * 4, sums = refs + kAttnRows * 4;
+    float f[N], sum[N], top = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        f[p] = attn_peer(refs, p);
+        sum[p] = attn_peer(sums, p);
+    }
+#pragma unroll
+    for (int p = 0; p < N; ++p) top = fmaxf(top, f[p]);
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        f[p] = f[p] == top ? 1.f : attn_exp2((f[p] - top) * sl);
+        if (sum[p] != 0.f) l += f[p] * sum[p];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+    for (int d = rank * kShare; d < (rank + 1) * kShare; d += kStep) {
+        float o[kStep] = {}, v[N][kStep];
+#pragma unroll
+        for (int p = 0; p < N; ++p)
+#pragma unroll
+            for (int e = 0; e < kStep; ++e) v[p][e] = attn_peer(part + ((d + e) * kAttnRows + row) * 4, p);
+#pragma unroll
+        for (int p = 0; p < N; ++p)
+#pragma unroll
+            for (int e = 0; e < kStep; ++e)
+                if (sum[p] != 0.f) o[e] = fmaf(f[p], v[p][e], o[e]);       // a part without keys has no O
+#pragma unroll
+        for (int e = 0; e < kStep; e += 4)
+            *reinterpret_cast<uint2 *>(dst + d + e) = make_uint2(h2_bits(__floats2half2_rn(o[e] * inv, o[e + 1] * inv)),
+                                                                 h2_bits(__floats2half2_rn(o[e + 2] * inv, o[e + 3] * inv)));
+    }
+}
+
+// SPLIT: an item's keys are shared between the CTAs of a cluster, a CTA has one item.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q,
                                                                       const __grid_constant__ CUtensorMap map_k,
                                                                       const __grid_constant__ CUtensorMap map_v,
@@ -332,6 +395,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
 
     // item number k of this CTA, from the schedule; false: there is none
     int q0, k0, nq, nk, row0, head, n_t[2], n;
+    [[maybe_unused]] int first_tile = 0;         // of this CTA's part of the keys
+    const int share = SPLIT ? (int)(blockIdx.x % (unsigned)a.splits) : 0;
+    auto j0 = [&]() { return SPLIT ? first_tile : 0; };
     auto take = [&](int k) {
         wait(item_full(k & 1), (uint32_t)k >> 1);
         const uint32_t at = items + 32u * (k & 1);
@@ -351,10 +417,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             const int seen = a.causal ? min(max(last + 1 + nk - nq, 0), nk) : nk;
             n_t[t] = t < a.tiles && last >= first ? (seen + kAttnKeys - 1) / kAttnKeys : 0;
         }
+        if constexpr (SPLIT) {                     // this CTA's part of the keys
+            const int each = (n_t[0] + a.splits - 1) / a.splits;
+            first_tile = min(share * each, n_t[0]);
+            n_t[0] = min(each, n_t[0] - first_tile);
+        }
         n = max(n_t[0], n_t[1]);
         return ok && any != 0;
     };
 
+    __half *joined = nullptr;                   // of this thread's row, where the keys are split
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -380,8 +452,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                 for (int c = 0; c < 4; ++c) attn_ld32(s_tm + 32 * c, r[c]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) attn_ld_wait(r[c]);
-                if (j * kAttnKeys + kAttnKeys > all_seen) {
-                    const int left = seen - j * kAttnKeys;
+                if ((j + j0()) * kAttnKeys + kAttnKeys > all_seen) {
+                    const int left = seen - (j + j0()) * kAttnKeys;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -457,28 +529,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             const float inv = l == 0.f ? 0.f : 1.f / l;
             __half *dst = a.out + (long long)(q0 + row) * a.ld_out + head * D;
             const bool valid = t < a.tiles && row < nq;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
+            if constexpr (SPLIT) {
+                if (t == 1) continue;               // a second query tile: there is none
+                // the part of the result goes to the ring, whose tiles have all been used
+                const uint32_t at = ring + (threadIdx.x & 127) * 4, refs = at + D * kAttnRows * 4;
                 if (mine > 0) {
-                    attn_ld32(o_tm + 32 * c, o);
-                    attn_ld_wait(o);
-                }
-                if (c == D / 32 - 1 && mine > 0) {
-                    // all of O is in registers or on its way out: the next item's products may start
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        attn_ld32(o_tm + 32 * c, o);
+                        attn_ld_wait(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + (32 * c + i) * kAttnRows * 4), "r"(o[i]) : "memory");
+                    }
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     arrive(o_empty(t));
                 }
-                if (valid) {
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(refs), "f"(ref) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(refs + kAttnRows * 4), "f"(l) : "memory");
+                if (valid) joined = dst;
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (mine > 0) {
+                        attn_ld32(o_tm + 32 * c, o);
+                        attn_ld_wait(o);
+                    }
+                    if (c == D / 32 - 1 && mine > 0) {
+                        // all of O is in registers or on its way out: the next item's products may start
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        arrive(o_empty(t));
+                    }
+                    if (valid) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v[4];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t v[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = l == 0.f ? 0u
-                                            : h2_bits(__floats2half2_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                                                        __uint_as_float(o[8 * i + 2 * e + 1]) * inv));
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = l == 0.f ? 0u
+                                                : h2_bits(__floats2half2_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                                            __uint_as_float(o[8 * i + 2 * e + 1]) * inv));
+                            *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
                     }
                 }
             }
@@ -518,7 +612,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                 if (!ok) break;
                 if (lane == 0) {
                     expect(full(s), C::kTile);
-                    tile(ring + s * C::kTile, (j & 1) ? &map_v : &map_k, kv_head, k0 + (j >> 1) * kAttnKeys, full(s));
+                    tile(ring + s * C::kTile, (j & 1) ? &map_v : &map_k, kv_head, k0 + ((j >> 1) + j0()) * kAttnKeys, full(s));
                 }
             }
             if (!ok) break;
@@ -587,7 +681,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             for (int j = 0; j < n && ok; ++j) {
                 const int iv = base + 2 * j + 1, ik = iv + 1;
                 sync_wait(full(iv % S), (uint32_t)(iv / S));
-                const int keys = min(kAttnKeys, nk - j * kAttnKeys), steps = (keys + 15) / 16;
+                const int keys = min(kAttnKeys, nk - (j + j0()) * kAttnKeys), steps = (keys + 15) / 16;
                 if (keys < 16 * steps && ok) {
                     // rows behind the end within the last step: zero, whatever follows the sequence (both warps write
                     // the same zeros)
@@ -636,7 +730,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
         __syncwarp();
     } else if (warp == 11) {
         // ----------------------------------------------------------- schedule
-        int id = blockIdx.x;
+        int id = SPLIT ? (int)(blockIdx.x / (unsigned)a.splits) : (int)blockIdx.x;
         for (int k = 0;; ++k) {
             const PromptItem it = id >= 0 ? prompt_item(a, id, a.tiles * kAttnRows) : PromptItem{};
             // a CTA without an item: the list is shorter than the grid, and so are all that follow
@@ -652,34 +746,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             }
             __syncwarp();
             if (!it.any) break;
-            // the next item is taken when this one's loads have been issued: earlier, it would wait here while other
-            // CTAs run out of work
-            wait(wanted, (uint32_t)k);
-            if (!ok) break;
-            if (lane == 0) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(answered) : "memory");
+            if constexpr (SPLIT) {                 // a cluster has one item
+                id = -1;
+            } else {
+                // the next item is taken when this one's loads have been issued: earlier, it would wait here while other
+                // CTAs run out of work
+                wait(wanted, (uint32_t)k);
+                if (!ok) break;
+                if (lane == 0) {
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(answered) : "memory");
+                    asm volatile(
+                        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                            answer),
+                        "r"(answered) : "memory");
+                }
+                wait(answered, (uint32_t)k);
+                if (!ok) break;
+                uint32_t got, x;
                 asm volatile(
-                    "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                        answer),
-                    "r"(answered) : "memory");
+                    "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+                    "ld.shared.b128 r, [%2];\n\t"
+                    "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                    "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                    "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+                    : "=r"(got), "=r"(x)
+                    : "r"(answer)
+                    : "memory");
+                // the answer has been read before the next one may be written over it
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                id = got ? (int)x : -1;
             }
-            wait(answered, (uint32_t)k);
-            if (!ok) break;
-            uint32_t got, x;
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
-                "ld.shared.b128 r, [%2];\n\t"
-                "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-                "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
-                : "=r"(got), "=r"(x)
-                : "r"(answer)
-                : "memory");
-            // the answer has been read before the next one may be written over it
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            id = got ? (int)x : -1;
         }
+    }
+    __syncwarp();
+    if constexpr (SPLIT) {
+        attn_cluster_sync();
+        if (joined) {
+            const int r = threadIdx.x & 127;
+            if (a.splits == 2) attn_join<D, 2>(ring, r, share, a.scale_log2, joined);
+            else if (a.splits == 4) attn_join<D, 4>(ring, r, share, a.scale_log2, joined);
+            else attn_join<D, 8>(ring, r, share, a.scale_log2, joined);
+        }
+        __syncwarp();
+        attn_cluster_sync();
     }
     __syncthreads();
     if (warp == 8) {

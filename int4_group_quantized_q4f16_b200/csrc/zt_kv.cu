@@ -174,13 +174,21 @@ bool tma_map_heads(CUtensorMap *map, const uint16_t *base, int D, int heads, int
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Where the items of one query tile fill at most half of the SMs, the keys of an item are split between the CTAs of a
+// cluster (2, 4 or 8), at least this many (of the average sequence) to each.  Whole and split: 137 queries, 2724 keys, 32
+// heads of 96, 40.4 and 26.7 us; 20 queries, 32020 keys, 32 heads of 128, 406 and 104; 64 queries, 32 heads, 1064 keys 20.3
+// and 14.5, 564 keys 13.5 and 12.1; 64 queries, 8 heads, 464 keys 11.7 and 11.9.  With 256 and 512 keys at least: 964 keys
+// of 8 heads 14.9 and 18.0, with 128 11.3.
+constexpr int kSplitKeys = 128;
+
 template <int D>
 int launch_prompt(PromptArgs &a, const uint16_t *q, int ld_q, const uint16_t *k, int ld_k, const uint16_t *v, int ld_v,
                   void *stream)
 {
     using C = PromptCfg<D>;
     int sms = 0;
-    if (resident_ctas(reinterpret_cast<const void *>(&prompt_attn_kernel<D>), kAttnThreads, C::kSmem, sms) < 1)
+    if (resident_ctas(reinterpret_cast<const void *>(&prompt_attn_kernel<D, false>), kAttnThreads, C::kSmem, sms) < 1 ||
+        resident_ctas(reinterpret_cast<const void *>(&prompt_attn_kernel<D, true>), kAttnThreads, C::kSmem, sms) < 1)
         return ZT_ERR_DEVICE;
     const int kv_heads = a.q_heads / a.group;
     CUtensorMap mq, mk, mv;
@@ -199,21 +207,27 @@ int launch_prompt(PromptArgs &a, const uint16_t *q, int ld_q, const uint16_t *k,
         return ((int64_t)a.total_q + tiles * kAttnRows - 1) / (tiles * kAttnRows) * a.q_heads;
     };
     a.tiles = items(2) < sms ? 1 : 2;
-    // every sequence may end with a partial block; CTAs without an item end at once
-    const int64_t grid = items(a.tiles) + (int64_t)(a.n_seqs - 1) * a.q_heads;
+    // Every sequence may end with a partial block; CTAs without an item end at once.
+    int64_t grid = items(a.tiles) + (int64_t)(a.n_seqs - 1) * a.q_heads;
+    a.splits = 1;
+    while (a.splits < kAttnSplits && grid * a.splits * 2 <= sms && keys >= (int64_t)a.n_seqs * a.splits * 2 * kSplitKeys) a.splits *= 2;
+    grid *= a.splits;
     if (grid > INT_MAX) return ZT_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kAttnThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.splits > 1 ? 2 : 1;
     clear_stale_error();
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_attn_kernel<D>, mq, mk, mv, (const PromptArgs &)a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, a.splits > 1 ? prompt_attn_kernel<D, true> : prompt_attn_kernel<D, false>, mq, mk, mv, (const PromptArgs &)a);
     return e == cudaSuccess ? ZT_OK : device_error(e, ZT_ERR_LAUNCH);
 }
 

@@ -204,3 +204,31 @@ def test_prompt_sink(zt, at):
     got = run(zt, q, k, v, [1], [n + 1], causal=False, scale=26 * np.log(2) / D)
     want = 2.0**-9 / (1 + 2.0**-9)
     assert (np.abs(got.astype(np.float64) - want) <= (2.0**-6 + 2.0**-9) * want).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,heads,kv", [(64, 2, 2), (96, 6, 2), (128, 8, 1), (64, 40, 8)])
+@pytest.mark.parametrize("nq,nk", [([5], [5000]), ([137], [2724]), ([1], [9000]), ([130, 2, 0], [6000, 37, 3000]),
+                                   ([3, 64], [4500, 0]), ([300], [1100])])
+def test_prompt_few_rows_long_keys(zt, D, heads, kv, nq, nk, causal):
+    """Few query tiles: the keys of each are split between CTAs, parts without keys or with a ragged end among them."""
+    rng = np.random.default_rng(D + heads + sum(nk))
+    q, k, v = fp16(rng, sum(nq), heads, D, by=1.5), fp16(rng, sum(nk), kv, D), fp16(rng, sum(nk), kv, D)
+    check(run(zt, q, k, v, nq, nk, causal), q, k, v, nq, nk, causal, D ** -0.5, heads=sorted({0, heads // 2, heads - 1}))
+
+
+def test_prompt_split_keys_that_are_not_seen(zt):
+    """NaN in a long sequence's keys reaches the rows that see them, whichever part they are in; keys behind the sequence do not."""
+    rng = np.random.default_rng(11)
+    D, n = 64, 8000
+    q, k, v = fp16(rng, 130, 1, D), fp16(rng, n + 300, 1, D), fp16(rng, n + 300, 1, D)
+    k[n:] = np.nan
+    v[n:] = np.inf
+    k[n - 65] = np.nan                   # the row that this key belongs to and those behind it see it
+    import torch
+    cu_q, cu_k = offsets([130]), np.array([0, n], np.int32)
+    plan = zt.PromptAttention(cuda(q), cuda(k), cuda(v), cuda(cu_q), cuda(cu_k), causal=True)
+    got = plan.run().cpu().numpy()
+    assert plan.errors() == 0
+    assert np.array_equal(np.isnan(got[:, 0]).all(1), np.arange(130) >= 65) and not np.isnan(got[:65]).any()
+    check(got[:65], q[:65], k[:n - 65], v[:n - 65], [65], [n - 65], True, D ** -0.5)
