@@ -43,8 +43,9 @@
 //
 // What bounds it.  One token of 131071 cached ones, 8 kv heads of 128, 4 query heads each
 // (151 MB of cache): 46.5 us, 3.2 TB/s; the copies alone, without the products, 25.7 us.  The
-// main loop is bound by issue slots: a pair of tiles takes a warp about 600 instructions, most
-// of them unpacking codes for the two products.  Joining the warps takes 2 us of it and joining
+// main loop is bound by issue slots and the chains between them (55 % of the slots busy over the
+// whole launch, the ALU pipe 45 %, memory 33 %): a pair of tiles takes a warp about 600
+// instructions, most of them unpacking codes for the two products.  Joining the warps takes 2 us of it and joining
 // the CTAs 5 us, most of that latency.  61 sequences of up to 6001 tokens (174 MB): 57 us; 7
 // sequences of up to 3999 tokens, 32 kv heads of 96, 4 query tokens (27 MB): 21 us; one sequence
 // of 517 tokens (1.8 MB): 8.0 us, of which streaming takes 4.1, the products 2.7 and the join 1.1.
