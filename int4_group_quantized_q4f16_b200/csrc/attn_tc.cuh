@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             const bool valid = t < a.tiles && row < nq;
             if constexpr (SPLIT) {
                 if (t == 1) continue;               // a second query tile: there is none
-                // the part of the result goes to the ring, whose tiles have all been used
+                // the part of the result goes to the ring, whose tiles have all been used: by warp 9, which O's completion
+                // covers; warp 10 only waits for them
                 const uint32_t at = ring + (threadIdx.x & 127) * 4, refs = at + D * kAttnRows * 4;
                 if (mine > 0) {
 #pragma unroll 1
@@ -682,9 +683,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                 const int iv = base + 2 * j + 1, ik = iv + 1;
                 sync_wait(full(iv % S), (uint32_t)(iv / S));
                 const int keys = min(kAttnKeys, nk - (j + j0()) * kAttnKeys), steps = (keys + 15) / 16;
-                if (keys < 16 * steps && ok) {
-                    // rows behind the end within the last step: zero, whatever follows the sequence (both warps write
-                    // the same zeros)
+                if (keys < 16 * steps && j < mine && ok) {
+                    // rows behind the end within the last step: zero, whatever follows the sequence.  Each warp does so
+                    // for its own products only (both write the same zeros): O's completion orders these stores before
+                    // the tile's next use, and where the keys are split that is tile 0's alone.
                     for (int c = lane; c < (16 * steps - keys) * C::kAtoms * 8; c += 32) {
                         const int row = keys + c / (C::kAtoms * 8), in = c % (C::kAtoms * 8);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(

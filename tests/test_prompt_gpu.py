@@ -217,6 +217,24 @@ def test_prompt_few_rows_long_keys(zt, D, heads, kv, nq, nk, causal):
     check(run(zt, q, k, v, nq, nk, causal), q, k, v, nq, nk, causal, D ** -0.5, heads=sorted({0, heads // 2, heads - 1}))
 
 
+@pytest.mark.parametrize("D,heads", [(64, 1), (96, 3), (128, 2), (128, 9)])
+@pytest.mark.parametrize("nk", [257, 513, 1001, 1025, 1535, 2050, 3079, 4093, 6157])
+def test_prompt_split_ragged_ends(zt, D, heads, nk):
+    """The part that holds a ragged end leaves its result in the shared memory where that end's V rows were zeroed: ends
+    in every 16-key step's middle, in parts of one to several tiles, infinities behind them, the same bits run after run."""
+    import torch
+    rng = np.random.default_rng(D + heads + nk)
+    q, k, v = fp16(rng, 40, heads, D, by=1.5), fp16(rng, nk + 130, 1, D), fp16(rng, nk + 130, 1, D)
+    k[nk:], v[nk:] = np.nan, np.inf
+    plan = zt.PromptAttention(cuda(q), cuda(k), cuda(v), cuda(offsets([40])), cuda(offsets([nk])), causal=False)
+    first = plan.run().clone()
+    check(first.cpu().numpy(), q, k[:nk], v[:nk], [40], [nk], False, D ** -0.5, heads=[0, heads - 1])
+    for _ in range(20):
+        plan._result.fill_(7.0)
+        assert torch.equal(plan.run(), first)
+    assert plan.errors() == 0
+
+
 def test_prompt_split_keys_that_are_not_seen(zt):
     """NaN in a long sequence's keys reaches the rows that see them, whichever part they are in; keys behind the sequence do not."""
     rng = np.random.default_rng(11)
