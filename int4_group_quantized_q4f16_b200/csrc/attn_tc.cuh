@@ -73,7 +73,7 @@ struct PromptCfg {
     static constexpr int kAtom = 128 * 128;                            // bytes
     static constexpr int kTile = kAtoms * kAtom;                       // 16 or 32 KB
     static constexpr int kStages = kAtoms == 2 ? 5 : 8;
-    static constexpr int kBars = 2 * kStages + 2 + 2 + 4 + 2 + 2 + 4 + 1 + 2 + 1;
+    static constexpr int kBars = 2 * kStages + 2 + 2 + 4 + 2 + 2 + 4 + 1 + 2 + 1 + 2;
     static constexpr int kItems = (kBars * 8 + 15) / 16 * 16;                           // two items of 32 bytes, the scheduler's answer
     static constexpr int kSmem = 2 * kTile + kStages * kTile + kItems + 64 + 16 + 16 + 1024;
     // kind::f16, D f32, A and B f16; the second product's B (V) is N-major (bit 16)
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
     auto item_empty = [&](int i) { return misc + 112u + 8u * i; };          // and read by its eleven readers
     const uint32_t answered = misc + 128u, wanted = misc + 152u;            // the scheduler's answer; an item's loads issued
     auto go = [&](int t) { return misc + 136u + 8u * t; };                  // tile t's turn at the exponentials
+    auto drain = [&](int t) { return misc + 160u + 8u * t; };               // tile t's products ended, after a wait ran out
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             init(o_full(t), 1);
             init(o_empty(t), 128);
             init(go(t), 128);
+            init(drain(t), 1);
             init(item_full(t), 1);
             init(item_empty(t), 11);
         }
@@ -726,8 +728,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             if (qs > 0) wait(q_empty, (uint32_t)(qs - 1));
             for (int i = max(0, base - S); i < base; ++i) wait(empty(i % S), (uint32_t)(i / S));
         } else if (attn_elect()) {
-            attn_commit(o_empty(t));                              // what was issued ends first: any free barrier will do
-            tc_wait(o_empty(t), 0u, false);
+            attn_commit(drain(t));                                // what was issued ends first
+            tc_wait(drain(t), 0u, false);
         }
         __syncwarp();
     } else if (warp == 11) {
