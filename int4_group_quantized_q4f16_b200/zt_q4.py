@@ -716,6 +716,8 @@ class KvAttention(_Launch):
     @staticmethod
     def _rows_of(t, dev, what, seqs, tokens, heads, dim):
         _on(t, dev, _torch().float16, what, 4)
+        if tuple(t.shape) != (seqs, tokens, heads, dim):
+            raise ValueError(f"{what} must be [{seqs}, {tokens}, {heads}, {dim}], is {tuple(t.shape)}")
         if tokens > 1 and seqs > 1 and t.stride(0) != tokens * t.stride(1):
             raise ValueError(f"the tokens of {what} must lie at one stride")
         row = t.stride(1) if tokens > 1 else t.stride(0)

@@ -159,6 +159,34 @@ def test_binding_refuses_host_tensors(zt):
         zt.KvCache(torch.zeros(1, 4, zt.kv_page_bytes(16, 2, 64), dtype=torch.uint8), 16, 2, 64)
 
 
+class OnDevice:
+    """A host tensor that says it is on a GPU, for the binding's checks (nothing is launched)."""
+
+    def __init__(self, t, device):
+        self._t, self.device, self.is_cuda = t, device, True
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    def as_strided(self, *args):
+        return OnDevice(self._t.as_strided(*args), self.device)
+
+
+def test_attention_refuses_an_out_of_another_shape(zt):
+    """An out with fewer sequences or other tokens than q is refused, also where the storage behind it would have room."""
+    import torch
+    dev, shape = torch.device("cuda", 0), (4, 2, 8, 64)
+    rows = lambda t: zt.KvAttention._rows_of(OnDevice(t, dev), dev, "out", *shape)   # noqa: E731
+    big = torch.zeros((8, 4, 16, 128), dtype=torch.float16)
+    assert rows(torch.zeros(shape, dtype=torch.float16))[1] == 8 * 64
+    for bad in (torch.zeros((8, 2, 8, 64), dtype=torch.float16)[:2], torch.zeros((8, 2, 8, 64), dtype=torch.float16)[:5],
+                torch.zeros((9, 1, 8, 64), dtype=torch.float16)[:4], torch.zeros((4, 4, 8, 64), dtype=torch.float16)[:, :1],
+                torch.zeros((4, 3, 8, 64), dtype=torch.float16), torch.zeros((2, 4, 8, 64), dtype=torch.float16),
+                big[:4, :2, :4, :64], big[:4, :2, :8, :96]):
+        with pytest.raises(ValueError, match="out"):
+            rows(bad)
+
+
 # ---------------------------------------------------------------- bookkeeping --
 def check(p: KvPages):
     """Every page's holders, recounted from the tables; pages being filled are held once."""
