@@ -427,7 +427,7 @@ typedef struct zt_q4_kv {
  * pos[i] < 0 marks padding: the row is skipped, what it would write is left as it was. */
 typedef struct zt_q4_kv_rows {
     const int32_t *seq, *pos;
-    int n;                    /* 0..2^24 */
+    int n;                    /* 0..2^24; 0: nothing is launched, and pointers to rows may be NULL */
     const int32_t *page_table;
     int n_seqs, max_pages;
 } zt_q4_kv_rows;

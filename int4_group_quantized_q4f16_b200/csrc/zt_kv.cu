@@ -59,10 +59,10 @@ int check_rows(const zt_q4_kv *kv, const zt_q4_kv_rows *rows)
     return check_table(rows->page_table, rows->n_seqs, rows->max_pages, kv->page_size);
 }
 
-// fp16 rows read and written 16 bytes at a time
-int check_matrix(const void *p, int ld, int64_t width)
+// fp16 rows read and written 16 bytes at a time; null is fine where there are none
+int check_matrix(const void *p, int ld, int64_t width, int rows = 1)
 {
-    if (!p || ld < width) return ZT_ERR_INVALID_ARG;
+    if ((!p && rows) || ld < width) return ZT_ERR_INVALID_ARG;
     return aligned(p, 16) && ld % 8 == 0 ? ZT_OK : ZT_ERR_MISALIGNED;
 }
 
@@ -244,7 +244,7 @@ int zt_q4_kv_append(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, const uint16_
     if (!rc) rc = check_rows(kv, rows);
     if (rc) return rc;
     const int64_t width = (int64_t)kv->kv_heads * kv->head_dim;
-    if ((rc = check_matrix(k, ld_k, width)) || (rc = check_matrix(v, ld_v, width))) return rc;
+    if ((rc = check_matrix(k, ld_k, width, rows->n)) || (rc = check_matrix(v, ld_v, width, rows->n))) return rc;
     if (rope) {
         if (!(rope->theta > 0.f) || rope->theta > 3.0e38f) return ZT_ERR_INVALID_ARG;
         if (rope->q) {
@@ -257,7 +257,7 @@ int zt_q4_kv_append(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, const uint16_
             return ZT_ERR_INVALID_ARG;
         }
         if (rope->k_out && (rc = check_matrix(rope->k_out, rope->ld_k_out, width))) return rc;
-        if (rope->k_out == k) return ZT_ERR_INVALID_ARG;
+        if (rope->k_out && rope->k_out == k) return ZT_ERR_INVALID_ARG;
     }
     if (rows->n == 0) return ZT_OK;
     KvAppendArgs a = {};
@@ -293,7 +293,7 @@ int zt_q4_kv_gather(const zt_q4_kv *kv, const zt_q4_kv_rows *rows, uint16_t *k, 
     if (!rc) rc = check_rows(kv, rows);
     if (rc) return rc;
     const int64_t width = (int64_t)kv->kv_heads * kv->head_dim;
-    if ((rc = check_matrix(k, ld_k, width)) || (rc = check_matrix(v, ld_v, width))) return rc;
+    if ((rc = check_matrix(k, ld_k, width, rows->n)) || (rc = check_matrix(v, ld_v, width, rows->n))) return rc;
     if (rows->n == 0) return ZT_OK;
     KvGatherArgs a = {};
     a.at = places(kv, rows->page_table, rows->n_seqs, rows->max_pages);

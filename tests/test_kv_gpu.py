@@ -262,6 +262,23 @@ def test_copy_pages(zt, layers):
     zt.KvCopy(cache, torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")).run()
 
 
+def test_calls_without_rows(zt):
+    """Empty tensors, with and without rotation: nothing is launched, nothing changes."""
+    import torch
+    rng = np.random.default_rng(14)
+    raw = rng.integers(0, 256, (3, zt.kv_page_bytes(16, 2, 64)), dtype=np.uint8)
+    cache = zt.KvCache(cuda(raw), 16, 2, 64)
+    x, no = cuda(fp16(rng, 5, 8, 64)), torch.empty(0, dtype=torch.int32, device="cuda")
+    table = cuda(np.zeros((1, 2), np.int32))
+    for part in (x[:0], x[2:2], x[5:]):
+        assert zt.KvAppend(cache, part[:, 4:6], part[:, 6:], no, no, table).run() == (None, None)
+        q, k = zt.KvAppend(cache, part[:, 4:6], part[:, 6:], no, no, table, q=part[:, :4], theta=1e4).run()
+        assert q.shape == (0, 4, 64) and k.shape == (0, 2, 64)
+        k, v = zt.KvGather(cache, no, no, table).run()
+        assert k.shape == v.shape == (0, 2, 64)
+    assert cache.errors() == 0 and np.array_equal(cache.pages[0].cpu().numpy(), raw)
+
+
 # ------------------------------------------------------------------ attention --
 LENS = [0, 1, 15, 16, 17, 33, 100, 257]
 

@@ -159,6 +159,21 @@ def test_binding_refuses_host_tensors(zt):
         zt.KvCache(torch.zeros(1, 4, zt.kv_page_bytes(16, 2, 64), dtype=torch.uint8), 16, 2, 64)
 
 
+def test_calls_without_rows_take_null_pointers(zt):
+    """An empty tensor's address is null: with n = 0 that is no fault, other arguments are still checked."""
+    app, gat, ref = zt.lib.zt_q4_kv_append, zt.lib.zt_q4_kv_gather, ctypes.byref
+    none = rows(zt, n=0, seq=None, pos=None)
+    assert app(ref(kv(zt)), ref(none), None, 128, None, 128, None, None) == zt.ZT_OK
+    assert gat(ref(kv(zt)), ref(none), None, 128, None, 128, None) == zt.ZT_OK
+    rope = zt.ZtKvRope(1e4, None, 256, 4, None, 256, None, 128)
+    assert app(ref(kv(zt)), ref(none), None, 128, None, 128, ref(rope), None) == zt.ZT_OK
+    assert app(ref(kv(zt, head_dim=80)), ref(none), None, 128, None, 128, None, None) == zt.ZT_ERR_UNSUPPORTED
+    assert app(ref(kv(zt)), ref(none), FAKE + 8, 128, None, 128, None, None) == zt.ZT_ERR_MISALIGNED
+    for call in (lambda: app(ref(kv(zt)), ref(rows(zt)), None, 128, FAKE, 128, None, None),
+                 lambda: gat(ref(kv(zt)), ref(rows(zt)), FAKE, 128, None, 128, None)):
+        assert call() == zt.ZT_ERR_INVALID_ARG
+
+
 class OnDevice:
     """A host tensor that says it is on a GPU, for the binding's checks (nothing is launched)."""
 
