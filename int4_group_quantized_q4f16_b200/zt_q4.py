@@ -529,11 +529,20 @@ def _on(t, device, dtype, what, dim):
         raise ValueError(f"{what} must be a {dim}-D {dtype} CUDA tensor on {device}")
 
 
+def _c_int(n, what):
+    """n, which ctypes would cut off where a C int cannot hold it."""
+    if n > 2**31 - 1:
+        raise ValueError(f"{what} is {n}, more than a 32-bit integer holds")
+    return n
+
+
 def _ints(t, device, what, dim=1, numel=None):
     torch = _torch()
     _on(t, device, torch.int32, what, dim)
     if not t.is_contiguous() or (numel is not None and t.numel() != numel):
         raise ValueError(f"{what} must be contiguous" + (f" with {numel} elements" if numel is not None else ""))
+    for n in t.shape:
+        _c_int(n, f"a dimension of {what}")
     return t.data_ptr()
 
 
@@ -547,7 +556,7 @@ def _heads(t, device, what, rows, heads, dim):
         raise ValueError(f"{what} must be [{rows}, {heads}, {dim}], is {tuple(t.shape)}")
     if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or (rows > 1 and t.stride(0) < heads * dim):
         raise ValueError(f"the heads of a row of {what} must lie side by side, rows behind each other")
-    return t.data_ptr(), int(t.stride(0)) if rows > 1 else heads * dim
+    return t.data_ptr(), _c_int(int(t.stride(0)), f"the row stride of {what}") if rows > 1 else heads * dim
 
 
 class _Launch:

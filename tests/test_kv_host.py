@@ -202,6 +202,25 @@ def test_attention_refuses_an_out_of_another_shape(zt):
             rows(bad)
 
 
+def test_binding_refuses_what_an_int_cannot_hold(zt):
+    """Strides, rows and table widths beyond the C call's 32-bit integers are refused, not cut off."""
+    import torch
+    dev = torch.device("cuda", 0)
+    meta = lambda *a, **k: OnDevice(torch.empty_strided(*a, device="meta", **k), dev)   # noqa: E731
+    half = dict(dtype=torch.float16)
+    assert zt._heads(meta((2, 4, 64), (2**31 - 8, 64, 1), **half), dev, "k", 2, 4, 64)[1] == 2**31 - 8
+    for stride in (2**31, 2**32 + 256):
+        with pytest.raises(ValueError, match="k"):
+            zt._heads(meta((2, 4, 64), (stride, 64, 1), **half), dev, "k", 2, 4, 64)
+    cache = zt.KvCache.__new__(zt.KvCache)
+    cache.device = dev
+    ints = lambda *shape: meta(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=torch.int32)   # noqa: E731
+    assert cache._rows(ints(3), ints(3), ints(2, 5)).n == 3
+    for seq, table in ((2**32 + 3, (2, 5)), (3, (2, 2**32 + 1)), (3, (2**31, 1))):
+        with pytest.raises(ValueError):
+            cache._rows(ints(seq), ints(seq), ints(*table))
+
+
 # ---------------------------------------------------------------- bookkeeping --
 def check(p: KvPages):
     """Every page's holders, recounted from the tables; pages being filled are held once."""
