@@ -559,22 +559,67 @@ def _heads(t, device, what, rows, heads, dim):
     return t.data_ptr(), _c_int(int(t.stride(0)), f"the row stride of {what}") if rows > 1 else heads * dim
 
 
+class _Fill:
+    """The zero-fill of a buffer that this module allocated, on the stream that was current then.  The caller does not see the
+    buffer, so runs on other streams are ordered behind its fill here."""
+
+    def __init__(self, device):
+        torch = _torch()
+        with torch.cuda.device(device):
+            stream = torch.cuda.current_stream()
+            self.captured = torch.cuda.is_current_stream_capturing()
+            self.event = torch.cuda.Event()
+            self.event.record(stream)
+        self.ordered = {stream.cuda_stream}       # handles of the streams that come behind the fill
+
+    def order(self, stream, capturing) -> bool:
+        """Makes `stream` wait for the fill; whether that holds for its later work too."""
+        if stream.cuda_stream in self.ordered:
+            return True
+        if self.captured and not capturing:
+            raise RuntimeError("a plan or cache made while a graph was captured can run in that capture only")
+        if capturing:
+            # a fill outside the capture cannot be waited for here: torch.cuda.graph waits for the device before it begins
+            if self.captured:
+                stream.wait_event(self.event)
+            return False
+        stream.wait_event(self.event)
+        self.ordered.add(stream.cuda_stream)
+        return True
+
+
 class _Launch:
     """A call whose arguments are checked and marshalled once; run() only launches, on the tensors' device and its
-    current stream (or `stream`).  The tensors are kept alive; their contents are read at run()."""
+    current stream (or `stream`).  The tensors are kept alive; their contents are read at run().  A first run on another
+    stream than the one that was current when the plan (or its cache) was made waits for what was filled there.  A run in a
+    capture does not: begin it when that stream has been waited for (torch.cuda.graph does), and keep the plan as long as
+    the graph."""
 
-    def __init__(self, name, device, args, keep, result):
+    def __init__(self, name, device, args, keep, result, fills):
         torch = _torch()
         self._fn, self._name, self._args, self._keep, self._result = getattr(lib, name), name, args, keep, result
-        self._device, self._index = device, device.index
+        self._device, self._index, self._fills = device, device.index, fills
+        self._ordered = set.intersection(*(f.ordered for f in fills))
         # the raw handle: building torch's Stream object takes longer than a launch
         self._current, self._raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+    def _order(self, handle):
+        torch = _torch()
+        # (an external stream of handle 0 would be another one than the default stream)
+        stream = torch.cuda.ExternalStream(handle, device=self._device) if handle else torch.cuda.default_stream(self._device)
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if all([f.order(stream, capturing) for f in self._fills]):
+            self._ordered.add(handle)
 
     def run(self, stream=None):
         if self._current() != self._index:
             with _torch().cuda.device(self._device):
                 return self.run(stream)
-        rc = self._fn(*self._args, self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+        handle = self._raw_stream(self._index) if stream is None else _stream_handle(stream)
+        if handle not in self._ordered:
+            self._order(handle)
+        rc = self._fn(*self._args, handle)
         if rc != ZT_OK:
             raise ZtError(rc, self._name)
         return self._result
@@ -598,6 +643,7 @@ class KvCache:
         self.layers, self.n_pages, self.page_bytes = (int(n) for n in pages.shape)
         self.page_size, self.kv_heads, self.head_dim = page_size, kv_heads, head_dim
         self.err = torch.zeros((1,), dtype=torch.int32, device=self.device)
+        self._fill = _Fill(self.device)
 
     @classmethod
     def empty(cls, layers: int, n_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -658,7 +704,7 @@ class KvAppend(_Launch):
         super().__init__("zt_q4_kv_append", dev,
                          (ctypes.byref(kv), ctypes.byref(rows), kp, ld_k, vp, ld_v,
                           ctypes.byref(rope) if rope else None),
-                         (cache, k, v, seq, pos, table, q, q_out, k_out, kv, rows, rope), (q_out, k_out))
+                         (cache, k, v, seq, pos, table, q, q_out, k_out, kv, rows, rope), (q_out, k_out), (cache._fill,))
 
 
 class KvGather(_Launch):
@@ -674,7 +720,7 @@ class KvGather(_Launch):
         kp, ld_k = _heads(k, dev, "k", n, cache.kv_heads, dim)
         vp, ld_v = _heads(v, dev, "v", n, cache.kv_heads, dim)
         super().__init__("zt_q4_kv_gather", dev, (ctypes.byref(kv), ctypes.byref(rows), kp, ld_k, vp, ld_v),
-                         (cache, seq, pos, table, k, v, kv, rows), (k, v))
+                         (cache, seq, pos, table, k, v, kv, rows), (k, v), (cache._fill,))
 
 
 class KvCopy(_Launch):
@@ -686,7 +732,8 @@ class KvCopy(_Launch):
         kv = cache._struct(0)
         super().__init__("zt_q4_kv_copy_pages", cache.device,
                          (ctypes.byref(kv), _ints(src, cache.device, "src", 1, n), _ints(dst, cache.device, "dst", 1, n), n,
-                          cache.layers, cache.n_pages * cache.page_bytes), (cache, src, dst, kv), cache.pages)
+                          cache.layers, cache.n_pages * cache.page_bytes), (cache, src, dst, kv), cache.pages,
+                         (cache._fill,))
 
 
 class KvAttention(_Launch):
@@ -710,8 +757,10 @@ class KvAttention(_Launch):
         if int(table.shape[0]) != seqs:
             raise ValueError(f"table has {table.shape[0]} rows for {seqs} sequences")
         nbytes = kv_attention_workspace_bytes(cache.kv_heads, heads, dim, tokens)
+        fills = (cache._fill,)
         if workspace is None:
             workspace = torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+            fills += (_Fill(dev),)
         _on(workspace, dev, torch.uint8, "workspace", 1)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
@@ -720,7 +769,7 @@ class KvAttention(_Launch):
                           _ints(table, dev, "table", 2), seqs, int(table.shape[1]),
                           float(dim ** -0.5 if scale is None else scale), op, ld_out, workspace.data_ptr(),
                           workspace.numel()),
-                         (cache, q, lens, table, out, workspace, kv), out)
+                         (cache, q, lens, table, out, workspace, kv), out, fills)
 
     @staticmethod
     def _rows_of(t, dev, what, seqs, tokens, heads, dim):
@@ -757,7 +806,7 @@ class PromptAttention(_Launch):
                          (qp, ld_q, kp, ld_k, vp, ld_v, _ints(cu_q, dev, "cu_q"), _ints(cu_k, dev, "cu_k", 1, seqs + 1), seqs,
                           total_q, total_k, heads, kv_heads, dim, int(bool(causal)),
                           float(dim ** -0.5 if scale is None else scale), op, ld_o, self.err.data_ptr()),
-                         (q, k, v, cu_q, cu_k, out), out)
+                         (q, k, v, cu_q, cu_k, out), out, (_Fill(dev),))
 
     def errors(self) -> int:
         v = ctypes.c_uint(0)

@@ -455,6 +455,85 @@ def test_graph_stream_and_workspace(zt):
     torch.cuda.synchronize()
 
 
+def test_runs_on_other_streams_wait_for_the_fills(zt):
+    """A workspace, an error word and a cache's memory that are zeroed behind long work on the constructing stream: a run on
+    another stream comes after it, whatever the memory held before."""
+    import torch
+    rng = np.random.default_rng(15)
+    lens = [6000]
+    cache, pool, table = filled(zt, rng, lens, 64, 1, 64)
+    q, ld, td = cuda(fp16(rng, 1, 1, 1, 64)), cuda(np.array(lens, np.int32)), cuda(table)
+    out, side = torch.empty_like(q), torch.cuda.Stream()
+    want = zt.KvAttention(cache, q, ld, td).run().clone()
+    x, zero = cuda(fp16(rng, 1, 2, 64)), cuda(np.zeros(1, np.int32))
+    sizes = (zt.kv_attention_workspace_bytes(1, 1, 64, 1), 2 * zt.kv_page_bytes(16, 1, 64), 4)
+    torch.cuda.synchronize()
+    dirty = [torch.full((n,), 0xEE, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    del dirty
+    torch.cuda._sleep(200_000_000)                  # about 0.1 s
+    plan = zt.KvAttention(cache, q, ld, td, out=out)
+    other = zt.KvCache.empty(1, 2, 16, 1, 64)
+    append = zt.KvAppend(other, x[:, :1], x[:, 1:], zero, zero, zero[None])
+    plan.run(stream=side)
+    append.run(stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(out, want) and cache.errors() == 0
+    raw = ref.Pool(np.zeros((2, other.page_bytes), np.uint8), 16, 1, 64)
+    raw.write(0, 0, x[0, :1].cpu().numpy(), x[0, 1:].cpu().numpy())
+    torch.cuda.synchronize()
+    same_bytes(other, raw)
+    assert other.errors() == 0
+
+
+def test_run_on_the_default_stream_waits_for_a_fill_on_another(zt):
+    import torch
+    rng = np.random.default_rng(17)
+    lens = [6000]
+    cache, pool, table = filled(zt, rng, lens, 64, 1, 64)
+    q, ld, td = cuda(fp16(rng, 1, 1, 1, 64)), cuda(np.array(lens, np.int32)), cuda(table)
+    out, side = torch.empty_like(q), torch.cuda.Stream()
+    want = zt.KvAttention(cache, q, ld, td).run().clone()
+    with torch.cuda.stream(side):
+        dirty = torch.full((zt.kv_attention_workspace_bytes(1, 1, 64, 1),), 0xEE, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        del dirty
+        torch.cuda._sleep(200_000_000)
+        plan = zt.KvAttention(cache, q, ld, td, out=out)
+    plan.run()
+    got = out.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and cache.errors() == 0
+
+
+def test_plans_made_in_a_capture(zt):
+    """A plan made while a graph is captured has its fill in the graph: it runs there, on a forked stream too, and is refused
+    outside."""
+    import torch
+    rng = np.random.default_rng(16)
+    lens = [3000]
+    cache, pool, table = filled(zt, rng, lens, 64, 1, 64)
+    q, ld, td = cuda(fp16(rng, 1, 1, 1, 64)), cuda(np.array(lens, np.int32)), cuda(table)
+    want = zt.KvAttention(cache, q, ld, td).run().clone()
+    outs = [torch.empty_like(q) for _ in range(2)]
+    main, fork, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        fork.wait_stream(main)
+        plans = [zt.KvAttention(cache, q, ld, td, out=o) for o in outs]
+        plans[0].run()
+        plans[1].run(stream=fork)
+        main.wait_stream(fork)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs) and cache.errors() == 0
+    with pytest.raises(RuntimeError, match="captured"):
+        plans[0].run()
+
+
 def test_attention_refuses_other_workspaces(zt):
     import torch
     cache = zt.KvCache.empty(1, 4, 16, 2, 64)
