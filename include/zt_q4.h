@@ -403,8 +403,8 @@ ZT_API int zt_q4_gemm_f16w_gate_up_silu(const uint16_t *w16, const uint16_t *x, 
  * or sequence out of range sets bit 0 (ZT_Q4_KV_ERR_PLACE) of *err and that row
  * or tile is left out; bit 1 (ZT_Q4_KV_ERR_WAIT) reports a bounded wait (2 s)
  * that ran out.  err (DEVICE, 4-byte aligned, may be NULL) is only ever OR-ed
- * into: the caller clears it, once, and reads it when it likes
- * (zt_q4_kv_errors, synchronous).
+ * into: the caller clears it, once, and reads it when the work in
+ * question has finished (zt_q4_kv_errors, synchronous).
  *
  * The kernels of this section read nothing before the kernel ahead of them on
  * the stream has completed.
@@ -527,7 +527,8 @@ ZT_API int zt_q4_prompt_attention(const uint16_t *q, int ld_q, const uint16_t *k
                                   int total_k, int q_heads, int kv_heads, int head_dim, int causal, float scale,
                                   uint16_t *out, int ld_out, uint32_t *err, void *stream);
 
-/* Synchronous read of an error word (kv->err or the err of zt_q4_prompt_attention). */
+/* Synchronous read of an error word (kv->err or the err of zt_q4_prompt_attention), of finished work: a copy on the
+ * legacy default stream, which streams made with cudaStreamNonBlocking are not ordered with. */
 ZT_API int zt_q4_kv_errors(const uint32_t *err, unsigned int *out);
 
 /*

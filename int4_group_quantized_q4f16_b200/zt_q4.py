@@ -559,6 +559,14 @@ def _heads(t, device, what, rows, heads, dim):
     return t.data_ptr(), _c_int(int(t.stride(0)), f"the row stride of {what}") if rows > 1 else heads * dim
 
 
+def _errors(err) -> int:
+    """An error word when everything launched on its device has finished (torch's streams are not ordered with the copy)."""
+    v = ctypes.c_uint(0)
+    _torch().cuda.synchronize(err.device)
+    _check(lib.zt_q4_kv_errors(err.data_ptr(), ctypes.byref(v)), "zt_q4_kv_errors")
+    return int(v.value)
+
+
 class _Fill:
     """The zero-fill of a buffer that this module allocated, on the stream that was current then.  The caller does not see the
     buffer, so runs on other streams are ordered behind its fill here."""
@@ -628,7 +636,8 @@ class _Launch:
 class KvCache:
     """A paged 4-bit KV cache (layout and quantization: include/zt_q4.h) over `pages`, a uint8 CUDA tensor
     [layers, n_pages, page_bytes] (or [n_pages, page_bytes] for one layer) that the caller owns.  A device error word
-    collects indices out of range; errors() reads it (synchronous), clear_errors() resets it."""
+    collects indices out of range; errors() reads it when the device's work has finished, clear_errors() resets it on the
+    current stream."""
 
     def __init__(self, pages, page_size: int, kv_heads: int, head_dim: int):
         torch = _torch()
@@ -664,9 +673,7 @@ class KvCache:
                         _ints(table, self.device, "table", 2), int(table.shape[0]), int(table.shape[1]))
 
     def errors(self) -> int:
-        v = ctypes.c_uint(0)
-        _check(lib.zt_q4_kv_errors(self.err.data_ptr(), ctypes.byref(v)), "zt_q4_kv_errors")
-        return int(v.value)
+        return _errors(self.err)
 
     def clear_errors(self) -> None:
         self.err.zero_()
@@ -788,7 +795,7 @@ class PromptAttention(_Launch):
     (rows may be strided: views into a QKV buffer), cu_q and cu_k int32 [n_seqs + 1] offsets of the sequences.  Causal:
     query i of a sequence with nq queries and nk keys sees the first i + 1 + nk - nq keys; a query that sees none gets
     zeros.  run() returns out, contiguous when not given.  scale defaults to head_dim ** -0.5.  errors() reads the error
-    word (synchronous; 0 unless a bounded wait ran out)."""
+    word when the device's work has finished (0 unless a bounded wait ran out)."""
 
     def __init__(self, q, k, v, cu_q, cu_k, causal: bool = True, out=None, scale=None):
         torch = _torch()
@@ -809,6 +816,4 @@ class PromptAttention(_Launch):
                          (q, k, v, cu_q, cu_k, out), out, (_Fill(dev),))
 
     def errors(self) -> int:
-        v = ctypes.c_uint(0)
-        _check(lib.zt_q4_kv_errors(self.err.data_ptr(), ctypes.byref(v)), "zt_q4_kv_errors")
-        return int(v.value)
+        return _errors(self.err)

@@ -506,6 +506,19 @@ def test_run_on_the_default_stream_waits_for_a_fill_on_another(zt):
     assert torch.equal(got, want) and cache.errors() == 0
 
 
+def test_errors_waits_for_other_streams(zt):
+    """A bad page met on a stream that is still busy is in the word that errors() returns."""
+    import torch
+    cache = zt.KvCache.empty(1, 4, 16, 1, 64)
+    x, zero = torch.ones((1, 1, 64), dtype=torch.float16, device="cuda"), cuda(np.zeros(1, np.int32))
+    append = zt.KvAppend(cache, x, x, zero, zero, cuda(np.full((1, 1), 99, np.int32)))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    append.run(stream=side)
+    assert cache.errors() == zt.ZT_Q4_KV_ERR_PLACE
+
+
 def test_plans_made_in_a_capture(zt):
     """A plan made while a graph is captured has its fill in the graph: it runs there, on a forked stream too, and is refused
     outside."""
