@@ -568,11 +568,13 @@ def _errors(err) -> int:
 
 
 class _Fill:
-    """The zero-fill of a buffer that this module allocated, on the stream that was current then.  The caller does not see the
-    buffer, so runs on other streams are ordered behind its fill here."""
+    """The zero-fill of buffers that this module allocated, on the stream that was current then.  The caller does not see the
+    buffers, so runs on other streams are ordered behind the fill here, and the allocator is told of them: memory that is
+    let go is not given to others before those runs have ended."""
 
-    def __init__(self, device):
+    def __init__(self, device, *tensors):
         torch = _torch()
+        self.tensors = tensors
         with torch.cuda.device(device):
             stream = torch.cuda.current_stream()
             self.captured = torch.cuda.is_current_stream_capturing()
@@ -586,6 +588,8 @@ class _Fill:
             return True
         if self.captured and not capturing:
             raise RuntimeError("a plan or cache made while a graph was captured can run in that capture only")
+        for t in self.tensors:
+            t.record_stream(stream)
         if capturing:
             # a fill outside the capture cannot be waited for here: torch.cuda.graph waits for the device before it begins
             if self.captured:
@@ -652,14 +656,16 @@ class KvCache:
         self.layers, self.n_pages, self.page_bytes = (int(n) for n in pages.shape)
         self.page_size, self.kv_heads, self.head_dim = page_size, kv_heads, head_dim
         self.err = torch.zeros((1,), dtype=torch.int32, device=self.device)
-        self._fill = _Fill(self.device)
+        self._fill = _Fill(self.device, self.err)
 
     @classmethod
     def empty(cls, layers: int, n_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
         """A cache on memory of its own (zeros: every place reads back as 0)."""
         torch = _torch()
-        return cls(torch.zeros((layers, n_pages, kv_page_bytes(page_size, kv_heads, head_dim)), dtype=torch.uint8,
-                               device=device), page_size, kv_heads, head_dim)
+        cache = cls(torch.zeros((layers, n_pages, kv_page_bytes(page_size, kv_heads, head_dim)), dtype=torch.uint8,
+                                device=device), page_size, kv_heads, head_dim)
+        cache._fill.tensors += (cache.pages,)
+        return cache
 
     def _struct(self, layer: int) -> ZtKv:
         if not 0 <= layer < self.layers:
@@ -767,7 +773,7 @@ class KvAttention(_Launch):
         fills = (cache._fill,)
         if workspace is None:
             workspace = torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=dev)
-            fills += (_Fill(dev),)
+            fills += (_Fill(dev, workspace),)
         _on(workspace, dev, torch.uint8, "workspace", 1)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
@@ -813,7 +819,7 @@ class PromptAttention(_Launch):
                          (qp, ld_q, kp, ld_k, vp, ld_v, _ints(cu_q, dev, "cu_q"), _ints(cu_k, dev, "cu_k", 1, seqs + 1), seqs,
                           total_q, total_k, heads, kv_heads, dim, int(bool(causal)),
                           float(dim ** -0.5 if scale is None else scale), op, ld_o, self.err.data_ptr()),
-                         (q, k, v, cu_q, cu_k, out), out, (_Fill(dev),))
+                         (q, k, v, cu_q, cu_k, out), out, (_Fill(dev, self.err),))
 
     def errors(self) -> int:
         return _errors(self.err)

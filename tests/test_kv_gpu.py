@@ -519,6 +519,35 @@ def test_errors_waits_for_other_streams(zt):
     assert cache.errors() == zt.ZT_Q4_KV_ERR_PLACE
 
 
+def test_dropped_plans_keep_their_memory_until_their_runs_end(zt):
+    """A plan (with its workspace) and a cache that are let go while their runs on another stream are still to come: memory
+    allocated afterwards on the constructing stream is not theirs."""
+    import torch
+    rng = np.random.default_rng(18)
+    lens = [6000]
+    cache, pool, table = filled(zt, rng, lens, 64, 1, 64)
+    q, ld, td = cuda(fp16(rng, 1, 1, 1, 64)), cuda(np.array(lens, np.int32)), cuda(table)
+    out, side = torch.empty_like(q), torch.cuda.Stream()
+    want = zt.KvAttention(cache, q, ld, td).run().clone()
+    x, zero = cuda(fp16(rng, 1, 2, 64)), cuda(np.zeros(1, np.int32))
+    own = zt.KvCache.empty(1, 2, 16, 1, 64)
+    plans = [zt.KvAttention(cache, q, ld, td, out=out), zt.KvAppend(own, x[:, :1], x[:, 1:], zero, zero, zero[None]),
+             zt.KvGather(own, zero, zero, zero[None])]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)              # about 0.1 s
+    for p in plans:
+        kv_back = p.run(stream=side)
+    sizes = (zt.kv_attention_workspace_bytes(1, 1, 64, 1), 2 * own.page_bytes, 4)
+    del plans, p, own
+    dirty = [torch.full((n,), 0xEE, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    side.synchronize()
+    assert torch.equal(out, want) and cache.errors() == 0
+    for got, src in zip(kv_back, (x[:, :1], x[:, 1:])):
+        assert np.array_equal(got.cpu().numpy(), ref.dequantize(*ref.quantize(src.cpu().numpy())).astype(np.float16))
+    assert all((d == 0xEE).all() for d in dirty)
+
+
 def test_plans_made_in_a_capture(zt):
     """A plan made while a graph is captured has its fill in the graph: it runs there, on a forked stream too, and is refused
     outside."""
