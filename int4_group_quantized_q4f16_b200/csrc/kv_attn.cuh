@@ -7,7 +7,10 @@
 //   p[t][c] = 2^(scale log2(e) S[t][c] - R[c])
 //   O[d][c] += sum_t (vc[t][d] - 7) (p[t][c] vs[t][g(d)])
 // and the result is O[d][c] / sum_t p[t][c].  kc and vc are the 4-bit codes, ks
-// and vs the fp16 scales of 32 values.
+// and vs the fp16 scales of 32 values.  q is multiplied by a power of two per column
+// first, which the column's softmax scale takes back: its largest value lies between
+// 2^14 and 2^16, so that neither q / 16 (below) nor x is rounded in fp16's subnormals
+// where q is small and the caller's scale large.
 //
 // Both products are mma.sync m16n8k16 with the codes as the A operand: a code
 // pair masked out of its word is a pair of fp16 subnormals (code * 2^-24, or
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
     uint32_t qf[G][4], xq;
     int seen[2];                 // tokens that columns 2j and 2j + 1 see
     float off = kKvOff;
-    const float sl = a.scale_log2 * 0x1p24f, inv_sl = 1.f / sl;
+    float sl[2];                 // softmax scale of columns 2j and 2j + 1, in the units of S as it is computed
     bool fresh = true, dead = false;
     int seg_tile0 = 0, step = 1, s = 0;
     uint32_t parity = 0;
@@ -540,11 +543,29 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             const int i = has ? col / a.group : 0, qh = h * a.group + (has ? col - i * a.group : 0);
             const __half *q = a.q + ((long long)seg.b * a.tokens + i) * a.ld_q + qh * D + 8 * j;
             __half xlo = __float2half_rn(0.f), xhi = xlo;
+            uint4 raw[G];
+            uint32_t top = 0u;                     // bit patterns of |q| go up with it; an infinity or a NaN lifts by 2^0
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const uint4 w = has ? *reinterpret_cast<const uint4 *>(q + 32 * g) : make_uint4(0, 0, 0, 0);
-                const float2 f0 = __half22float2(bits_h2(w.x)), f1 = __half22float2(bits_h2(w.y)),
-                             f2 = __half22float2(bits_h2(w.z)), f3 = __half22float2(bits_h2(w.w));
+                raw[g] = has ? *reinterpret_cast<const uint4 *>(q + 32 * g) : make_uint4(0, 0, 0, 0);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[g].x & 0x7FFF7FFFu, raw[g].y & 0x7FFF7FFFu),
+                                             __vmaxu2(raw[g].z & 0x7FFF7FFFu, raw[g].w & 0x7FFF7FFFu)));
+            }
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float largest = __half2float(__ushort_as_half((unsigned short)max(top & 0xFFFFu, top >> 16)));
+            const int lift = max(0, 14 + 127 - max((int)(__float_as_uint(largest) >> 23), 127 - 24));
+            const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                sl[e] = a.scale_log2 * __uint_as_float((uint32_t)(127 + 24 - __shfl_sync(0xffffffffu, lift, 4 * (2 * j + e))) << 23);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float2 f0 = __half22float2(bits_h2(raw[g].x)), f1 = __half22float2(bits_h2(raw[g].y)),
+                       f2 = __half22float2(bits_h2(raw[g].z)), f3 = __half22float2(bits_h2(raw[g].w));
+                f0.x *= up, f0.y *= up, f1.x *= up, f1.y *= up, f2.x *= up, f2.y *= up, f3.x *= up, f3.y *= up;
+                const uint4 w = make_uint4(h2_bits(__float22half2_rn(f0)), h2_bits(__float22half2_rn(f1)),      // exact
+                                           h2_bits(__float22half2_rn(f2)), h2_bits(__float22half2_rn(f3)));
                 float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -677,13 +698,13 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             if (__any_sync(0xffffffffu, large)) off = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2])) * sl;
+                float mx = fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2])) * sl[e];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const float ref = fmaxf(mx, R[e] + before) - off;
                 const float f = R[e] == ref ? 1.f : kv_exp2(R[e] - ref);
                 R[e] = ref;
-                most[e] = (ref + (off > 0.f ? kKvRoom : kKvRoomLarge)) * inv_sl;
+                most[e] = (ref + (off > 0.f ? kKvRoom : kKvRoomLarge)) * __frcp_rn(sl[e]);
                 L[e] *= f;
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m) {
@@ -697,8 +718,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
         const float r0 = R[0] == -INFINITY ? 0.f : R[0], r1 = R[1] == -INFINITY ? 0.f : R[1];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float p0 = kv_exp2(fmaf(P[u][0], sl, -r0)), p1 = kv_exp2(fmaf(P[u][1], sl, -r1));
-            const float p2 = kv_exp2(fmaf(P[u][2], sl, -r0)), p3 = kv_exp2(fmaf(P[u][3], sl, -r1));
+            const float p0 = kv_exp2(fmaf(P[u][0], sl[0], -r0)), p1 = kv_exp2(fmaf(P[u][1], sl[1], -r1));
+            const float p2 = kv_exp2(fmaf(P[u][2], sl[0], -r0)), p3 = kv_exp2(fmaf(P[u][3], sl[1], -r1));
             L[0] += p0 + p2;
             L[1] += p1 + p3;
             const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);

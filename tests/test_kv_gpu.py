@@ -365,6 +365,29 @@ def test_attention_value_ranges(zt, v_by):
     check_attention(zt, cache, pool, fp16(rng, 2, 1, 4, 128, by=2.0), lens, table, large_v=v_by > 1)
 
 
+@pytest.mark.parametrize("D,q_heads,heads,tokens", [(64, 4, 2, 1), (96, 6, 2, 3), (128, 8, 1, 1), (128, 16, 2, 2)])
+@pytest.mark.parametrize("by", [1e-3, 1e-4, 1e-5, 3e-7, 1.0, 2000.0, 16000.0])
+def test_attention_query_ranges(zt, D, q_heads, heads, tokens, by):
+    """Queries down to fp16's smallest values and up to its largest, with a scale that makes up for it: the scores are those of
+    queries near 1, and so is what a call may be off by (the powers of two that q and the scale exchange are exact)."""
+    rng = np.random.default_rng(D + tokens)
+    lens = [512, 37]
+    cache, pool, table = filled(zt, rng, lens, 32, heads, D)
+    q = np.clip(rng.standard_normal((2, tokens, q_heads, D)) * by, -65504, 65504).astype(np.float16)
+    check_attention(zt, cache, pool, q, lens, table, scale=2.0 / by * D ** -0.5)
+
+
+def test_attention_queries_of_different_sizes(zt):
+    """Heads of all sizes beside one another, values of all sizes within a head, a head of zeros."""
+    rng = np.random.default_rng(19)
+    lens, D = [700, 33, 2000], 96
+    cache, pool, table = filled(zt, rng, lens, 32, 1, D)
+    q = rng.standard_normal((3, 1, 9, D)) * np.array([1, 1e-1, 1e-2, 1e-3, 1e-4, 1e-5, 10, 0, 1])[:, None]
+    q[:, :, 8] *= 2.0 ** -rng.integers(0, 22, (3, 1, D))
+    check_attention(zt, cache, pool, q.astype(np.float16), lens, table, scale=0.5)
+    check_attention(zt, cache, pool, q[:, :, 2:6].astype(np.float16), lens, table, scale=300.0)
+
+
 def test_attention_sink(zt):
     """One token takes half the weight, thousands of others share the rest: none of it is lost."""
     rng = np.random.default_rng(7)
