@@ -799,7 +799,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                         dst[c * D + 16 * m + 8 + r] = O[m][e + 2] * 0x1p10f;
                     }
                     if (r == 0) {
-                        dst[C::kCols * D + c] = R[e];
+                        // without a reference, tokens were not seen, or all of their scores were NaN: those count
+                        dst[C::kCols * D + c] = l != l ? fmaxf(R[e], 0.f) : R[e];
                         dst[C::kCols * (D + 1) + c] = l;
                         reinterpret_cast<int *>(dst)[C::kPart] = seg.b;
                         reinterpret_cast<int *>(dst)[C::kPart + 1] = seg.hc;

@@ -388,6 +388,30 @@ def test_attention_queries_of_different_sizes(zt):
     check_attention(zt, cache, pool, q[:, :, 2:6].astype(np.float16), lens, table, scale=300.0)
 
 
+def test_attention_queries_that_are_not_finite(zt):
+    """A head with an infinity or a NaN gives NaN; the others are not touched by it."""
+    rng = np.random.default_rng(20)
+    lens, D = [300], 64
+    cache, pool, table = filled(zt, rng, lens, 32, 1, D)
+    q = fp16(rng, 1, 2, 5, D)
+    q[0, 0, 1, 7], q[0, 1, 3, 40], q[0, 1, 4, 0] = np.nan, np.nan, np.inf
+    got = check_attention(zt, cache, pool, q, lens, table)
+    assert np.isnan(got).any(-1).tolist() == [[[False, True, False, False, False], [False, False, False, True, True]]]
+
+
+@pytest.mark.parametrize("n", [20, 300, 7000])
+def test_attention_part_of_nan_scores(zt, n):
+    """Tokens whose scores are all NaN make up a warp's or a CTA's whole share of a sequence: the result is NaN all the same."""
+    rng = np.random.default_rng(21)
+    for lo, hi in ((0, 16), (n - 1, n), (n // 2, n // 2 + 1)):
+        def edit(b, p, k, v):
+            if lo <= p < hi:
+                k[0, 5] = np.inf
+        cache, pool, table = filled(zt, rng, [n], 16, 2, 64, edit=edit)
+        got = check_attention(zt, cache, pool, fp16(rng, 1, 1, 4, 64), [n], table)
+        assert np.isnan(got[0, 0, :2]).all() and np.isfinite(got[0, 0, 2:]).all()
+
+
 def test_attention_sink(zt):
     """One token takes half the weight, thousands of others share the rest: none of it is lost."""
     rng = np.random.default_rng(7)
