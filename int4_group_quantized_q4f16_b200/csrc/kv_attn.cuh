@@ -4,7 +4,7 @@
 // Mathematics.  For a kv head, the columns are its (query token, query head)
 // pairs; per tile of 16 cached tokens
 //   S[t][c] = sum_g ks[t][g] sum_{d in g} kc[t][d] q[d][c]  +  sum_g ks[t][g] x[g][c],   x[g][c] = -7 sum_{d in g} q[d][c]
-//   p[t][c] = 2^(scale log2(e) S[t][c] - R[c])
+//   p[t][c] = 2^(scale log2(e) (S[t][c] - M[c]) + 9)
 //   O[d][c] += sum_t (vc[t][d] - 7) (p[t][c] vs[t][g(d)])
 // and the result is O[d][c] / sum_t p[t][c].  kc and vc are the 4-bit codes, ks
 // and vs the fp16 scales of 32 values.  q is multiplied by a power of two per column
@@ -25,14 +25,16 @@
 // tcgen05 would need the unpacked codes written to shared memory first (4x the
 // cache's bytes); the work is bound by the cache's bytes.
 //
-// R is a reference, not the running maximum: the largest score when it was set, less
-// 9 (p = 2^9 there).  O and the sum of p are rescaled only when a score passes R by
-// 15.  That keeps p * vs in the upper range of fp16: with scales below 2 (values
-// below 14) p * vs stays under 2^16, and a weight of 2^-24 of the largest one still
-// has 2 bits.  A tile with a larger scale sets the two to 0 and 2 (p <= 4, p * vs <=
-// 4 * 65504 / 7).  p goes through the transpose as two fp16 parts, so that p * vs is
-// rounded once (with p rounded first, the error of a long sequence's output was 1.5
-// times that of its rounding to fp16 alone, not 1.3); sums of p and O are fp32.
+// M is a reference, not the running maximum: the largest score when it was set (p =
+// 2^9 there).  O and the sum of p are rescaled only when a score passes M by 5.5 / (scale
+// log2(e)).  That keeps p * vs in the upper range of fp16: with scales below 2 (values
+// below 14) p * vs stays under 2^15.5, and a weight of 2^-24 of the largest one still has
+// 2 bits.  A tile with a larger scale sets the 9 and the 5.5 to 0 and 2 (p <= 4, p * vs <=
+// 4 * 65504 / 7).  The difference is taken before the product with the scale: scores may
+// be of any size, and near M it is exact.  p goes through the transpose as two fp16
+// parts, so that p * vs is rounded once (with p rounded first, the error of a long
+// sequence's output was 1.5 times that of its rounding to fp16 alone, not 1.3); sums of p
+// and O are fp32.
 //
 // Work split.  The (sequence, kv head) segments are laid end to end in tiles, each
 // with four more that stand for its own cost, and cut into equal runs, one per CTA,
@@ -98,7 +100,7 @@ struct KvAttnCfg {
 // query tokens: with 1 48.6, 63.7 and 22.5 us, 2 48.5, 56.9 and 20.8, 4 46.5, 57.0 and 20.9, 8 46.7, 57.3 and 20.7.
 constexpr int kKvSegTiles = 4;
 constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
-constexpr float kKvOff = 9.f, kKvRoom = 15.f, kKvRoomLarge = 2.f;
+constexpr float kKvOff = 9.f, kKvRoom = 5.5f, kKvRoomLarge = 2.f;
 
 // Runs of tiles: CTA c of n takes total / n of them, the first total % n CTAs one more.
 struct KvRuns {
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
         for (int s = 0; s < C::kPairs && to_copy > 0; ++s) issue(s);
     }
 
-    float O[D / 16][4], R[2], L[2], most[2];
+    float O[D / 16][4], minus_m[2], L[2], most[2];      // -M (0 without one); largest score without a rescale (-inf)
     uint32_t qf[G][4], xq;
     int seen[2];                 // tokens that columns 2j and 2j + 1 see
     float off = kKvOff;
@@ -590,8 +592,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                 for (int e = 0; e < 4; ++e) O[m][e] = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                R[e] = most[e] = -INFINITY;
-                L[e] = 0.f;
+                most[e] = -INFINITY;
+                minus_m[e] = L[e] = 0.f;
                 seen[e] = seg.len - a.tokens + 1 + (c0 + 2 * j + e) / a.group;
             }
         }
@@ -636,10 +638,10 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                        qf[g][1], 0.f, 0.f, 0.f, 0.f);
                 kv_mma(d, wa[g] & 0x00F000F0u, wb[g] & 0x00F000F0u, ha & 0x00F000F0u, hb & 0x00F000F0u, qf[g][2],
                        qf[g][3], d[0], d[1], d[2], d[3]);
-                p[0] = g ? fmaf(sc.x, d[0], p[0]) : sc.x * d[0];
-                p[1] = g ? fmaf(sc.x, d[1], p[1]) : sc.x * d[1];
-                p[2] = g ? fmaf(sc.y, d[2], p[2]) : sc.y * d[2];
-                p[3] = g ? fmaf(sc.y, d[3], p[3]) : sc.y * d[3];
+                const uint64_t lo = f2_pack(sc.x, sc.x), hi = f2_pack(sc.y, sc.y), d01 = f2_pack(d[0], d[1]), d23 = f2_pack(d[2], d[3]);
+                const float2 p01 = f2_split(g ? f2_fma(lo, d01, f2_pack(p[0], p[1])) : f2_mul(lo, d01));
+                const float2 p23 = f2_split(g ? f2_fma(hi, d23, f2_pack(p[2], p[3])) : f2_mul(hi, d23));
+                p[0] = p01.x, p[1] = p01.y, p[2] = p23.x, p[3] = p23.y;
             }
             float z[4];
             kv_mma(z, za, zb, 0u, 0u, xq, 0u, 0.f, 0.f, 0.f, 0.f);
@@ -698,13 +700,13 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             if (__any_sync(0xffffffffu, large)) off = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2])) * sl[e];
+                float mx = fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2]));
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const float ref = fmaxf(mx, R[e] + before) - off;
-                const float f = R[e] == ref ? 1.f : kv_exp2(R[e] - ref);
-                R[e] = ref;
-                most[e] = (ref + (off > 0.f ? kKvRoom : kKvRoomLarge)) * __frcp_rn(sl[e]);
+                const float old = most[e] == -INFINITY ? -INFINITY : -minus_m[e], now = fmaxf(old, mx);
+                const float f = kv_exp2(old == now ? off - before : fmaf(old - now, sl[e], off - before));
+                minus_m[e] = now == -INFINITY ? 0.f : -now;
+                most[e] = __fmaf_rd(off > 0.f ? kKvRoom : kKvRoomLarge, __frcp_rn(sl[e]), now);
                 L[e] *= f;
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m) {
@@ -714,14 +716,15 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             }
         }
         uint32_t pt[2][2], pl[2][2];      // the weights as B fragments: rounded, and what the rounding left
-        // a column that has seen nothing yet keeps R = -inf: its weights are 2^-inf = 0
-        const float r0 = R[0] == -INFINITY ? 0.f : R[0], r1 = R[1] == -INFINITY ? 0.f : R[1];
+        const uint64_t m2 = f2_pack(minus_m[0], minus_m[1]), sl2 = f2_pack(sl[0], sl[1]), off2 = f2_pack(off, off);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float p0 = kv_exp2(fmaf(P[u][0], sl[0], -r0)), p1 = kv_exp2(fmaf(P[u][1], sl[1], -r1));
-            const float p2 = kv_exp2(fmaf(P[u][2], sl[0], -r0)), p3 = kv_exp2(fmaf(P[u][3], sl[1], -r1));
-            L[0] += p0 + p2;
-            L[1] += p1 + p3;
+            const float2 x01 = f2_split(f2_fma(f2_add(f2_pack(P[u][0], P[u][1]), m2), sl2, off2));
+            const float2 x23 = f2_split(f2_fma(f2_add(f2_pack(P[u][2], P[u][3]), m2), sl2, off2));
+            const float p0 = kv_exp2(x01.x), p1 = kv_exp2(x01.y), p2 = kv_exp2(x23.x), p3 = kv_exp2(x23.y);
+            const float2 sums = f2_split(f2_add(f2_pack(L[0], L[1]), f2_add(f2_pack(p0, p1), f2_pack(p2, p3))));
+            L[0] = sums.x;
+            L[1] = sums.y;
             const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
             const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
             pt[u][0] = kv_transpose(h2_bits(h01));
@@ -800,7 +803,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                     }
                     if (r == 0) {
                         // without a reference, tokens were not seen, or all of their scores were NaN: those count
-                        dst[C::kCols * D + c] = l != l ? fmaxf(R[e], 0.f) : R[e];
+                        const float ref = most[e] == -INFINITY ? most[e] : -fmaf(minus_m[e], sl[e], off);
+                        dst[C::kCols * D + c] = l != l ? fmaxf(ref, 0.f) : ref;
                         dst[C::kCols * (D + 1) + c] = l;
                         reinterpret_cast<int *>(dst)[C::kPart] = seg.b;
                         reinterpret_cast<int *>(dst)[C::kPart + 1] = seg.hc;

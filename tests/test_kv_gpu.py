@@ -412,6 +412,45 @@ def test_attention_part_of_nan_scores(zt, n):
         assert np.isnan(got[0, 0, :2]).all() and np.isfinite(got[0, 0, 2:]).all()
 
 
+@pytest.mark.parametrize("n", [300, 7000])
+@pytest.mark.parametrize("scale", [2.0**-8, 2.0**-4, 0.125, 1.0, 2.0**20, 2.0**60])
+def test_attention_scores_of_any_size(zt, n, scale):
+    """Scores up to 2^90, each of them exact in fp32 (a common value times small whole numbers), some equal: the largest ones
+    share the weight, all others lie too far below to count, and nothing overflows."""
+    rng = np.random.default_rng(22)
+    c = rng.permutation(np.r_[np.full(n - n // 3, 512), np.full(n // 3 - 5, 1023), np.full(5, 1024)]).astype(np.float16)
+
+    def edit(b, p, k, v):
+        k[:] = c[p]
+    cache, pool, table = filled(zt, rng, [n], 16, 1, 64, edit=edit)
+    q = np.full((1, 1, 3, 64), 1024, np.float16)
+    q[0, 0, 1:] = np.float16([[-1024], [16384]])
+    check_attention(zt, cache, pool, q, [n], table, scale=scale)
+
+
+@pytest.mark.parametrize("scale", [0.5, 0.3, 0.7, 1.1])
+def test_attention_weights_at_the_largest_scale_below_two(zt, scale):
+    """V scales of 1.999 and weights as far above the reference as they come without a rescale, at scores of up to 2^17 in the
+    exponent, whose roundings are 2^-7: weight * V scale is fp16's largest value nearly.  All V are alike, so the output is
+    V's value whatever the weights; it is off by their product's rounding and its own, 2^-11 each, and fp32 sums."""
+    rng = np.random.default_rng(23)
+    D, heads, seqs, page = 64, 16, 40, 80
+    k, v = np.zeros((page, heads, D), np.float16), np.full((page, heads, D), 15.992, np.float16)
+    k[:, :, 0], k[64:, :, 32:] = 64.0, 1.0
+    pool = ref.Pool(np.zeros((1, zt.kv_page_bytes(page, heads, D)), np.uint8), page, heads, D)
+    for p in range(page):
+        pool.write(0, p, k[p], v[p])
+    cache = zt.KvCache(cuda(pool.raw.reshape(1, -1)), page, heads, D)
+    q = np.zeros((seqs, 16, heads, D), np.float16)
+    q[..., 0] = rng.uniform(100, 2**17 * np.log(2) / 64 / scale, q.shape[:-1])
+    q[..., 32:40] = 6 * np.log(2) / scale / 8                   # later tokens: 6 powers of two more ...
+    q[..., 40] = rng.uniform(-0.03, 0.03, q.shape[:-1])         # ... and a little
+    out = zt.KvAttention(cache, cuda(q), cuda(np.full(seqs, page, np.int32)), cuda(np.zeros((seqs, 1), np.int32)), scale=scale).run()
+    want = pool.values([0], page)[1][0, 0, 0]
+    assert want == 8 * np.float64(np.float16(1.999))
+    assert (np.abs(out.cpu().numpy() - want) <= (2.0**-10 + 2.0**-16) * want).all() and cache.errors() == 0
+
+
 def test_attention_sink(zt):
     """One token takes half the weight, thousands of others share the rest: none of it is lost."""
     rng = np.random.default_rng(7)
