@@ -8,7 +8,8 @@
 // nor l is rescaled.  p is rounded to fp16 for the second product, and the 7 keeps it
 // in the upper range: of many small weights beside a large one those down to 2^-21 of
 // it are rounded like normal numbers, and 2^-31 is not zero yet (2^-14 and 2^-24
-// without).  Scores, m, l and O are fp32.
+// without).  Scores, m, l and O are fp32.  Where scale log2(e) m is so large that its
+// rounding would count (2^18), m is taken off the scores first.
 //
 // Layout.  A CTA takes two tiles of 128 queries of one head (one where that leaves
 // SMs idle) and walks the keys.  Both products are tcgen05.mma (M = 128, kind::f16):
@@ -55,6 +56,7 @@ constexpr int kAttnRows = 128, kAttnKeys = 128;
 constexpr int kAttnThreads = 384;
 constexpr float kAttnSlack = 8.f;      // scores above the reference before a rescale, in powers of two
 constexpr float kAttnLift = 7.f;       // log2 of a weight at the reference
+constexpr float kAttnFar = 0x1p18f;    // exponents whose reference is taken off the scores before the product with the scale
 
 struct PromptArgs {
     __half *out;
@@ -444,7 +446,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             auto seen_by = [&](int r) { return a.causal ? min(max(r + 1 + nk - nq, 0), nk) : nk; };
             const int seen = seen_by(row), all_seen = seen_by(row0 + t * kAttnRows);      // by this row, by every row
             const int both = min(n_t[0], n_t[1]);
-            float ref = -INFINITY, l = 0.f;
+            float ref = -INFINITY, l = 0.f, base = 0.f;      // base: scale log2(e) ref - 7, 0 without one
+            bool far = false;                               // any row's of this warp is too large to be rounded
             for (int j = 0; j < mine && ok; ++j, ++turn) {
                 wait(s_full(t), turn);
                 if (!ok) break;
@@ -472,11 +475,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                     m4[c] = fmaxf(m4[c], __uint_as_float(r[c][31]));
                 }
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (__any_sync(0xffffffffu, mx > ref + slack)) {
+                if (__any_sync(0xffffffffu, mx > __fadd_rd(ref, slack))) {
                     const float to = fmaxf(ref, mx);
                     const float f = ref == to ? 1.f : attn_exp2((ref - to) * sl);
                     ref = to;
                     l *= f;
+                    base = ref == -INFINITY ? 0.f : ref * sl - kAttnLift;
+                    far = __any_sync(0xffffffffu, fabsf(base) > kAttnFar);
                     if (j > 0) {
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -489,7 +494,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                         }
                     }
                 }
-                const float base = ref == -INFINITY ? 0.f : ref * sl - kAttnLift;
+                float from = base;
+                if (__builtin_expect(far, 0)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) - (ref == -INFINITY ? 0.f : ref));
+                    from = -kAttnLift;
+                }
                 // The two groups take turns at the exponentials: in step, both would wait for them and then both for
                 // the products.
                 const bool paired = j < both;
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                     ++pairs;
                     if (!ok) break;
                 }
-                const uint64_t sl2 = f2_pack(sl, sl), base2 = f2_pack(-base, -base);
+                const uint64_t sl2 = f2_pack(sl, sl), base2 = f2_pack(-from, -from);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {

@@ -138,6 +138,19 @@ def test_prompt_rescales(zt):
     check(run(zt, q, k, v, [n], [n], scale=0.1), q, k, v, [n], [n], True, 0.1)
 
 
+@pytest.mark.parametrize("nq,nk", [(600, 600), (5, 5000)])
+@pytest.mark.parametrize("scale", [2.0**-8, 2.0**-4, 0.125, 1.0, 2.0**20, 2.0**60])
+def test_prompt_scores_of_any_size(zt, nq, nk, scale):
+    """Scores up to 2^90, each of them exact in fp32 (a common value times small whole numbers), some equal: the largest ones
+    that a row sees share the weight, all others lie too far below to count, and nothing overflows."""
+    rng = np.random.default_rng(13)
+    c = rng.permutation(np.r_[np.full(nk - nk // 3, 512), np.full(nk // 3 - 5, 1023), np.full(5, 1024)])
+    q = np.full((nq, 3, 64), 1024, np.float16)
+    q[:, 1], q[:, 2] = -1024, 16384
+    k, v = np.broadcast_to(c[:, None, None], (nk, 1, 64)).astype(np.float16), fp16(rng, nk, 1, 64)
+    check(run(zt, q, k, v, [nq], [nk], scale=scale), q, k, v, [nq], [nk], True, scale)
+
+
 def test_prompt_bad_offsets_are_left_out(zt):
     """Offsets that decrease or leave the tensors: those sequences count as empty, nothing else is touched."""
     import torch
