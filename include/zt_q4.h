@@ -482,7 +482,8 @@ ZT_API int zt_q4_kv_copy_pages(const zt_q4_kv *kv, const int32_t *src, const int
  * token gives zeros.  n_seqs <= ZT_Q4_KV_MAX_SEQS; q_heads a multiple of kv_heads;
  * scale between 2^-64 and 2^64.
  * Scores, softmax statistics and sums are fp32; the products of the weights and V's
- * scales are rounded to fp16.  out may not overlap q or the pool.
+ * scales are rounded to fp16, with the largest weight at 2^9 (at 2^(13 - e), if that is
+ * less, where scales of 2^e are among them: values of 2^(e + 3) and more).  out may not overlap q or the pool.
  * workspace: DEVICE, 16-byte aligned, zt_q4_kv_attention_workspace_bytes() bytes
  * (a function of these sizes alone).  Unlike the other workspaces of this library
  * it must be ZERO-FILLED before its first use: it holds counters that every call

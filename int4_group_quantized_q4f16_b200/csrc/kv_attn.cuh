@@ -29,8 +29,8 @@
 // 2^9 there).  O and the sum of p are rescaled only when a score passes M by 5.5 / (scale
 // log2(e)).  That keeps p * vs in the upper range of fp16: with scales below 2 (values
 // below 14) p * vs stays under 2^15.5, and a weight of 2^-24 of the largest one still has
-// 2 bits.  A tile with a larger scale sets the 9 and the 5.5 to 0 and 2 (p <= 4, p * vs <=
-// 4 * 65504 / 7).  The difference is taken before the product with the scale: scores may
+// 2 bits.  From the first tile with a scale of 2^e or more on, e > 0, the room is e less,
+// first at the cost of the 5.5, down to 1.5, then of the 9.  The difference is taken before the product with the scale: scores may
 // be of any size, and near M it is exact.  p goes through the transpose as two fp16
 // parts, so that p * vs is rounded once (with p rounded first, the error of a long
 // sequence's output was 1.5 times that of its rounding to fp16 alone, not 1.3); sums of p
@@ -100,7 +100,7 @@ struct KvAttnCfg {
 // query tokens: with 1 48.6, 63.7 and 22.5 us, 2 48.5, 56.9 and 20.8, 4 46.5, 57.0 and 20.9, 8 46.7, 57.3 and 20.7.
 constexpr int kKvSegTiles = 4;
 constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
-constexpr float kKvOff = 9.f, kKvRoom = 5.5f, kKvRoomLarge = 2.f;
+constexpr float kKvOff = 9.f, kKvRoom = 14.5f, kKvSlack = 1.5f;
 
 // Runs of tiles: CTA c of n takes total / n of them, the first total % n CTAs one more.
 struct KvRuns {
@@ -266,6 +266,21 @@ struct KvCursor {
 
 // b's halves, zero where p's are.  Kept out of line: it is hardly ever needed.
 static __device__ __noinline__ uint32_t kv_hide(uint32_t b, uint32_t p) { return b & ~__vcmpeq2(p, 0u); }
+
+// Largest V scale among a lane's, as fp16 bits; a NaN counts as the largest number: columns that see it are lost, and others
+// it is hidden from in a sequence's last tiles only.  Out of line: for scales of 2 and more.
+template <int N>
+struct KvScales {
+    uint32_t w[N];
+};
+template <int N>
+static __device__ __noinline__ uint32_t kv_largest(KvScales<N> s)
+{
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = __vmaxu2(m, s.w[i] & 0x7FFF7FFFu);
+    return min(max(m & 0xFFFFu, m >> 16), 0x7BFFu);
+}
 
 // Columns of head-and-block hc.
 __device__ __forceinline__ int kv_columns(const KvAttnArgs &a, int hc, int kcols)
@@ -528,7 +543,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
     float O[D / 16][4], minus_m[2], L[2], most[2];      // -M (0 without one); largest score without a rescale (-inf)
     uint32_t qf[G][4], xq;
     int seen[2];                 // tokens that columns 2j and 2j + 1 see
-    float off = kKvOff;
+    float room = kKvRoom;             // less e, where 2^e is the largest power of two among the V scales so far (above 1)
+    auto off_of = [](float room) { return fminf(kKvOff, room - kKvSlack); };
     float sl[2];                 // softmax scale of columns 2j and 2j + 1, in the units of S as it is computed
     bool fresh = true, dead = false;
     int seg_tile0 = 0, step = 1, s = 0;
@@ -538,7 +554,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             // a new segment: its queries as B fragments, the zero point's term, the columns' ends
             fresh = false;
             seg_tile0 = seg.tile;
-            off = kKvOff;
+            room = kKvRoom;
             const int h = seg.hc / a.blocks, c0 = (seg.hc - h * a.blocks) * C::kCols;
             const int col = c0 + r;
             const bool has = col < a.cols;
@@ -555,8 +571,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             }
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float largest = __half2float(__ushort_as_half((unsigned short)max(top & 0xFFFFu, top >> 16)));
-            const int lift = max(0, 14 + 127 - max((int)(__float_as_uint(largest) >> 23), 127 - 24));
+            const float big = __half2float(__ushort_as_half((unsigned short)max(top & 0xFFFFu, top >> 16)));
+            const int lift = max(0, 14 + 127 - max((int)(__float_as_uint(big) >> 23), 127 - 24));
             const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -691,13 +707,25 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             mend = true;
         }
         const bool large = (any & 0x40004000u) != 0u;                // a scale of 2 or more
-        bool lift = large && off > 0.f;
+        bool lift = false;
+        uint32_t met = 0u;
+        if (__builtin_expect(large, 0)) {
+            KvScales<4 * G> all;
+#pragma unroll
+            for (int g = 0; g < 2 * G; ++g) {
+                all.w[g] = vs[0][g];
+                all.w[2 * G + g] = vs[1][g];
+            }
+            met = kv_largest(all);
+            lift = (float)(int)(met >> 10) > kKvRoom + 15.f - room;
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             lift |= fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2])) > most[e];
         if (__any_sync(0xffffffffu, lift)) {
-            const float before = off;
-            if (__any_sync(0xffffffffu, large)) off = 0.f;
+            const float before = off_of(room);
+            room = fminf(room, kKvRoom + 15.f - (float)(int)(__reduce_max_sync(0xffffffffu, met) >> 10));
+            const float off = off_of(room);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float mx = fmaxf(fmaxf(P[0][e], P[0][e + 2]), fmaxf(P[1][e], P[1][e + 2]));
@@ -706,7 +734,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                 const float old = most[e] == -INFINITY ? -INFINITY : -minus_m[e], now = fmaxf(old, mx);
                 const float f = kv_exp2(old == now ? off - before : fmaf(old - now, sl[e], off - before));
                 minus_m[e] = now == -INFINITY ? 0.f : -now;
-                most[e] = __fmaf_rd(off > 0.f ? kKvRoom : kKvRoomLarge, __frcp_rn(sl[e]), now);
+                most[e] = __fmaf_rd(room - off, __frcp_rn(sl[e]), now);
                 L[e] *= f;
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m) {
@@ -716,7 +744,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             }
         }
         uint32_t pt[2][2], pl[2][2];      // the weights as B fragments: rounded, and what the rounding left
-        const uint64_t m2 = f2_pack(minus_m[0], minus_m[1]), sl2 = f2_pack(sl[0], sl[1]), off2 = f2_pack(off, off);
+        const uint64_t m2 = f2_pack(minus_m[0], minus_m[1]), sl2 = f2_pack(sl[0], sl[1]), off2 = f2_pack(off_of(room), off_of(room));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const float2 x01 = f2_split(f2_fma(f2_add(f2_pack(P[u][0], P[u][1]), m2), sl2, off2));
@@ -803,7 +831,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                     }
                     if (r == 0) {
                         // without a reference, tokens were not seen, or all of their scores were NaN: those count
-                        const float ref = most[e] == -INFINITY ? most[e] : -fmaf(minus_m[e], sl[e], off);
+                        const float ref = most[e] == -INFINITY ? most[e] : -fmaf(minus_m[e], sl[e], off_of(room));
                         dst[C::kCols * D + c] = l != l ? fmaxf(ref, 0.f) : ref;
                         dst[C::kCols * (D + 1) + c] = l;
                         reinterpret_cast<int *>(dst)[C::kPart] = seg.b;

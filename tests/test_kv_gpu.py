@@ -451,6 +451,31 @@ def test_attention_weights_at_the_largest_scale_below_two(zt, scale):
     assert (np.abs(out.cpu().numpy() - want) <= (2.0**-10 + 2.0**-16) * want).all() and cache.errors() == 0
 
 
+@pytest.mark.parametrize("bits", [16, 18, 20, 22])
+@pytest.mark.parametrize("top", [16.5, 40.0, 300.0, 4000.0, 60000.0])
+def test_attention_small_weights_beside_a_large_value(zt, top, bits):
+    """Tokens of weight 2^-bits beside one whose V scale is 2^e or more, which a warp's whole run follows.  Their products with
+    their scale s = 0.3 are rounded at 2^off 2^-bits s, off = min(9, 13 - e): off by 2^-11 of themselves, or by half of fp16's
+    smallest step, 2^-25.  The output's own rounding is 2^-11 (2^-25 where it is subnormal), fp32 sums and scores 2^-16."""
+    rng = np.random.default_rng(24)
+    D, heads, n, seqs, page = 64, 8, 200, 600, 208
+    pool = ref.Pool(np.zeros((1, zt.kv_page_bytes(page, heads, D)), np.uint8), page, heads, D)
+    first = int(rng.integers(0, 16))
+    for p in range(n):
+        k, v = np.full((heads, D), 1.0 if p == first else 0.0, np.float16), np.full((heads, D), 2.4, np.float16)
+        if p == first:
+            v[:, :32], v[:, 32:] = 0.0, top
+        pool.write(0, p, k, v)
+    cache = zt.KvCache(cuda(pool.raw.reshape(1, -1)), page, heads, D)
+    k, v = pool.values([0], n)
+    q, scale = np.ones((seqs, 1, heads, D), np.float16), bits * np.log(2) / D
+    out = zt.KvAttention(cache, cuda(q), cuda(np.full(seqs, n, np.int32)), cuda(np.zeros((seqs, 1), np.int32)), scale=scale).run()
+    want, _ = ref.attention(q[0], k, v, [n], scale)
+    off = min(9, 13 - int(np.floor(np.log2(top / 8))))
+    tol = (2.0**-10 + 2.0**-16 + 2.0**-25 / (2.0**(off - bits) * 0.3)) * np.abs(want) + 2.0**-25
+    assert (np.abs(out.cpu().numpy()[:, 0].astype(np.float64) - want) <= tol).all() and cache.errors() == 0
+
+
 def test_attention_sink(zt):
     """One token takes half the weight, thousands of others share the rest: none of it is lost."""
     rng = np.random.default_rng(7)
