@@ -926,7 +926,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
         const float *base = a.part + (2ll * chain.x + 1) * C::kPart;      // the last part lies one slot earlier
         // warp w takes column w % cols, and of its parts every q-th: the W / cols warps of a column halve the
         // rounds of loads; what each has goes through shared memory (the rings are done with)
-        const int q = max(1, W / cols);
+        static_assert(W >= 2 * C::kCols, "two warps a column at least");
+        const int q = W / cols;
         float *slots = reinterpret_cast<float *>(rings);
 #pragma unroll 1
         for (int c = warp; c < cols * q; c += W) {
@@ -947,10 +948,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                 }
                 sum.add(R1, l1, v);
             }
-            if (q == 1) sum.store(kv_out_row(a, chain.z, chain.w, col, C::kCols, D));
-            else sum.leave(slots, c, W);
+            sum.leave(slots, c, W);
         }
-        if (q == 1) continue;
         __syncthreads();
         if (warp < cols) {
             KvSum<D> sum;
