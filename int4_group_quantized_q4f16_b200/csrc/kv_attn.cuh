@@ -581,15 +581,15 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
             for (int g = 0; g < G; ++g) {
                 float2 f0 = __half22float2(bits_h2(raw[g].x)), f1 = __half22float2(bits_h2(raw[g].y)),
                        f2 = __half22float2(bits_h2(raw[g].z)), f3 = __half22float2(bits_h2(raw[g].w));
+                float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
                 f0.x *= up, f0.y *= up, f1.x *= up, f1.y *= up, f2.x *= up, f2.y *= up, f3.x *= up, f3.y *= up;
                 const uint4 w = make_uint4(h2_bits(__float22half2_rn(f0)), h2_bits(__float22half2_rn(f1)),      // exact
                                            h2_bits(__float22half2_rn(f2)), h2_bits(__float22half2_rn(f3)));
-                float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 // lane j of a quad keeps the two groups of its k slots: groups 0..3 rounded to fp16 in
                 // slots 0..3, what the rounding left in slots 4..7 (2^-8 of them, so that none overflows)
-                sum *= -7.f * 0x1p-8f;
+                sum *= -7.f * 0x1p-8f * up;
                 const __half high = __float2half_rn(sum);
                 const __half part = j < 2 ? high : __float2half_rn(sum - __half2float(high));
                 if (g / 2 == (j & 1)) (g & 1 ? xhi : xlo) = part;
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                 const float old = most[e] == -INFINITY ? -INFINITY : -minus_m[e], now = fmaxf(old, mx);
                 const float f = kv_exp2(old == now ? off - before : fmaf(old - now, sl[e], off - before));
                 minus_m[e] = now == -INFINITY ? 0.f : -now;
-                most[e] = __fmaf_rd(room - off, __frcp_rn(sl[e]), now);
+                most[e] = __fadd_rd(now, __fdividef(room - off, sl[e]));      // the room has half a power of two to spare
                 L[e] *= f;
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m) {
