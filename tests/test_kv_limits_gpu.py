@@ -121,3 +121,63 @@ def test_many_rows(zt):
     some = rng.integers(0, len(seq), 2000)
     for got, src in ((k, x[:, :1]), (v, x[:, 1:])):
         assert np.array_equal(got.cpu().numpy()[some], ref.dequantize(*ref.quantize(src.cpu().numpy()[some])).astype(np.float16))
+
+
+@pytest.mark.parametrize("width", [4, 200])
+def test_replayed_step_follows_lengths_and_pages(zt, width):
+    """One captured decode step (append, then attention, whose launch goes by the table's width), replayed while lengths,
+    positions and the page table change: what eager calls on a copy of the cache give, bit for bit."""
+    import torch
+    rng = np.random.default_rng(width)
+    page, heads, D, lens = 16, 2, 64, np.array([14, 0, 31], np.int32)
+    cache, other = (zt.KvCache.empty(1, 12, page, heads, D) for _ in range(2))
+    table = cuda(np.zeros((3, width), np.int32))
+    x, q = cuda(fp16(rng, 3, 2 * heads, D)), cuda(fp16(rng, 3, 1, 4, D))
+    seq, pos, ld = cuda(np.arange(3, dtype=np.int32)), cuda(lens), cuda(lens + 1)
+
+    def plans(c):
+        return zt.KvAppend(c, x[:, :heads], x[:, heads:], seq, pos, table), zt.KvAttention(c, q, ld, table)
+    first, eager = plans(cache), plans(other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p in first:
+            p.run()
+    order = torch.from_numpy(rng.permutation(12).astype(np.int32)).cuda()
+    for step in range(20):
+        x.copy_(cuda(fp16(rng, 3, 2 * heads, D)))
+        q.copy_(cuda(fp16(rng, 3, 1, 4, D)))
+        pos.copy_(cuda(lens + step))
+        ld.copy_(cuda(lens + step + 1))
+        if step == 10:
+            ld[1] = 0                                # a padded place in the batch
+        table[:, :4] = order.view(3, 4)
+        graph.replay()
+        for p in eager:
+            p.run()
+        assert torch.equal(first[1]._result, eager[1]._result) and torch.equal(cache.pages, other.pages), step
+        assert step != 10 or not first[1]._result[1].any()
+    assert cache.errors() == 0 and other.errors() == 0
+
+
+def test_calls_at_once(zt):
+    """Decode steps and prompts side by side on streams of their own, again and again: each gives what it gives alone."""
+    import torch
+    rng = np.random.default_rng(34)
+    lens = [900, 5000, 1, 300]
+    cache, pool, table = kv.filled(zt, rng, lens, 32, 2, 128)
+    ld, td = cuda(np.array(lens, np.int32)), cuda(table)
+    plans = [zt.KvAttention(cache, cuda(fp16(rng, 4, t, 8, 128)), ld, td) for t in (1, 1, 4)]
+    for nq, nk in (([300, 40], [300, 700]), ([9], [5000])):
+        plans.append(zt.PromptAttention(cuda(fp16(rng, sum(nq), 4, 96)), cuda(fp16(rng, sum(nk), 2, 96)),
+                                        cuda(fp16(rng, sum(nk), 2, 96)), cuda(prompt.offsets(nq)), cuda(prompt.offsets(nk))))
+    want = [p.run().clone() for p in plans]
+    streams = [torch.cuda.Stream() for _ in plans]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for p, s in zip(plans, streams):
+            with torch.cuda.stream(s):
+                p._result.fill_(7.0)
+                p.run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p._result, w) for p, w in zip(plans, want))
+    assert cache.errors() == 0 and not any(p.errors() for p in plans[3:])
