@@ -9,7 +9,10 @@
 // in the upper range: of many small weights beside a large one those down to 2^-21 of
 // it are rounded like normal numbers, and 2^-31 is not zero yet (2^-14 and 2^-24
 // without).  Scores, m, l and O are fp32.  Where scale log2(e) m is so large that its
-// rounding would count (2^18), m is taken off the scores first.
+// rounding would count (2^18), m is taken off the scores first, in the rescale's branch,
+// which such rows take at every tile (in a branch of its own before the exponentials: 137
+// queries on 2724 keys 27.1 us, packed prompts 75.5, as here 26.9 and 74.4; without, for
+// smaller scores only, 26.7 and 75.2).
 //
 // Layout.  A CTA takes two tiles of 128 queries of one head (one where that leaves
 // SMs idle) and walks the keys.  Both products are tcgen05.mma (M = 128, kind::f16):
@@ -31,8 +34,9 @@
 // 1370 for the exponentials.  The groups take turns at the exponentials (without: 548 us,
 // with: 504).  Computing 1/8 .. 3/8 of them by polynomial on the fma units made it slower
 // (565 .. 647 us): the chain of one tile, not the exponentials' rate, sets the pace.
-// 8192 tokens causal: 504-527 us, 1040-1090 TFLOP/s; 784 before the groups took turns,
-// the products had a warp per tile and items were taken in order of their weight.
+// 8192 tokens causal: 484-527 us, 1040-1140 TFLOP/s, in bursts; 540-590 us, 930-1020 TFLOP/s,
+// call after call, where the power limit holds the clock near 1.5 GHz.  784 before the groups
+// took turns, the products had a warp per tile and items were taken in order of their weight.
 //
 // Schedule.  The grid has a CTA per work item (sequence, head, block of queries), the
 // heavy blocks first; a CTA that runs keeps taking items whose CTAs have not been
@@ -446,8 +450,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
             auto seen_by = [&](int r) { return a.causal ? min(max(r + 1 + nk - nq, 0), nk) : nk; };
             const int seen = seen_by(row), all_seen = seen_by(row0 + t * kAttnRows);      // by this row, by every row
             const int both = min(n_t[0], n_t[1]);
-            float ref = -INFINITY, l = 0.f, base = 0.f;      // base: scale log2(e) ref - 7, 0 without one
-            bool far = false;                               // any row's of this warp is too large to be rounded
+            // base: scale log2(e) ref - 7, 0 without one; limit: the largest score without a rescale
+            float ref = -INFINITY, l = 0.f, base = 0.f, limit = -INFINITY;
             for (int j = 0; j < mine && ok; ++j, ++turn) {
                 wait(s_full(t), turn);
                 if (!ok) break;
@@ -475,13 +479,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                     m4[c] = fmaxf(m4[c], __uint_as_float(r[c][31]));
                 }
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (__any_sync(0xffffffffu, mx > __fadd_rd(ref, slack))) {
+                if (__any_sync(0xffffffffu, mx > limit)) {
                     const float to = fmaxf(ref, mx);
                     const float f = ref == to ? 1.f : attn_exp2((ref - to) * sl);
                     ref = to;
                     l *= f;
                     base = ref == -INFINITY ? 0.f : ref * sl - kAttnLift;
-                    far = __any_sync(0xffffffffu, fabsf(base) > kAttnFar);
+                    limit = __fadd_rd(ref, slack);
+                    if (__any_sync(0xffffffffu, fabsf(base) > kAttnFar)) {
+                        // too large for some row: the references are taken off the scores, here at every tile
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) - (ref == -INFINITY ? 0.f : ref));
+                        base = -kAttnLift;
+                        limit = -INFINITY;
+                    }
                     if (j > 0) {
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -494,15 +508,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                         }
                     }
                 }
-                float from = base;
-                if (__builtin_expect(far, 0)) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) - (ref == -INFINITY ? 0.f : ref));
-                    from = -kAttnLift;
-                }
                 // The two groups take turns at the exponentials: in step, both would wait for them and then both for
                 // the products.
                 const bool paired = j < both;
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const __gr
                     ++pairs;
                     if (!ok) break;
                 }
-                const uint64_t sl2 = f2_pack(sl, sl), base2 = f2_pack(-from, -from);
+                const uint64_t sl2 = f2_pack(sl, sl), base2 = f2_pack(-base, -base);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
