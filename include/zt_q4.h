@@ -514,7 +514,8 @@ ZT_API int zt_q4_kv_attention(const zt_q4_kv *kv, const uint16_t *q, int ld_q, i
  * the inputs; scale between 2^-64
  * and 2^64.  Rows of out that no sequence covers are left as they were.
  * A sequence whose offsets decrease or leave total_q (total_k) is treated as one
- * without queries (keys).  Scores, softmax statistics and sums are fp32; the
+ * without queries (keys); those that remain must not share query rows (rows that
+ * two of them cover get either's result, or are left as they were).  Scores, softmax statistics and sums are fp32; the
  * weights are rounded to fp16 for the second product.  Keys that a query does not
  * see have weight zero in it, so a NaN or an infinity in v of a later token of the
  * same sequence can reach earlier queries of that sequence (0 * NaN); other

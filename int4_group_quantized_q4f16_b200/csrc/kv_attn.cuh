@@ -47,18 +47,22 @@
 // order of the tokens: results do not depend on timing.
 //
 // What bounds it.  One token of 131071 cached ones, 8 kv heads of 128, 4 query heads each
-// (151 MB of cache): 46.5 us, 3.2 TB/s; the copies alone, without the products, 25.7 us.  The
-// main loop is bound by issue slots and the chains between them (55 % of the slots busy over the
-// whole launch, the ALU pipe 45 %, memory 33 %): a pair of tiles takes a warp about 600
-// instructions, most of them unpacking codes for the two products.  Joining the warps takes 2 us of it and joining
-// the CTAs 5 us, most of that latency.  61 sequences of up to 6001 tokens (174 MB): 57 us; 7
-// sequences of up to 3999 tokens, 32 kv heads of 96, 4 query tokens (27 MB): 21 us; one sequence
-// of 517 tokens (1.8 MB): 8.0 us, of which streaming takes 4.1, the products 2.7 and the join 1.1.
-// Warps: 16 with two pairs of tiles in flight each; 8 with four pairs took 54.0, 67.2 and 22.4 us
-// on the first three.  Columns: eight at a time.  Sixteen that share a pass over the tiles (8 warps,
-// for the registers) took 30.1 us where two passes of eight take 24.0 (4 sequences of 20000 tokens,
-// 12 columns per kv head; 16 columns: 32.6 and 25.3), and were faster only where the cache is larger
-// than L2: 131071 tokens of 8 heads, 16 columns, 79.3 and 80.7; 32 sequences of 8000, 57.4 and 64.6.
+// (151 MB of cache): 47.0 us, 3.2 TB/s; the copies alone, without the products, 25.7 us.  The
+// main loop is bound by issue slots and the chains between them (56 % of the slots busy over the
+// whole launch, the ALU pipe 47 %, memory 34 %): a pair of tiles takes a warp about 600
+// instructions, most of them unpacking codes for the two products.  Joining the warps takes 2 us
+// of it and joining the CTAs 5 us, most of that latency.  61 sequences of up to 6001 tokens (174
+// MB): 57.5 us; 7 sequences of up to 3999 tokens, 32 kv heads of 96, 4 query tokens (27 MB): 20.9
+// us; one sequence of 517 tokens (1.8 MB): 8.15 us, of which streaming takes 4.1, the products 2.7
+// and the join 1.1.  Warps: 16 with two pairs of tiles in flight each; 8 with four pairs took 54.0,
+// 67.2 and 22.4 us on the first three (then 46.5, 57.0 and 20.9).  Columns: eight at a time.
+// Sixteen that share a pass over the tiles (8 warps, for the registers) took 30.1 us where two
+// passes of eight take 23.9 (4 sequences of 20000 tokens, 12 columns per kv head; 16 columns: 32.6
+// and 24.9), and were faster only where the cache is larger than L2: 131071 tokens of 8 heads, 16
+// columns, 79.3 and 81.8; 32 sequences of 8000, 57.4 and 65.0.
+// References, in us on the first two: a rounded product scale * M taken off in the multiply-add,
+// which holds for scores up to some thousands only, 46.5 and 57.0; with a branch for far ones 47.6
+// and 58.3 out of line, 48.1 and 58.9 in the loop; differences first, for any score, as above.
 #pragma once
 
 #include "kv_common.cuh"
@@ -97,7 +101,7 @@ struct KvAttnCfg {
 };
 
 // What starting and ending a segment costs, in tiles.  131071 tokens of 8 heads, 61 ragged sequences, 7 with 4
-// query tokens: with 1 48.6, 63.7 and 22.5 us, 2 48.5, 56.9 and 20.8, 4 46.5, 57.0 and 20.9, 8 46.7, 57.3 and 20.7.
+// query tokens: with 1 49.4, 63.4 and 22.8 us, 2 49.4, 57.5 and 20.9, 4 47.4, 57.7 and 20.9, 8 47.7, 58.0 and 20.7.
 constexpr int kKvSegTiles = 4;
 constexpr int kKvMaxCtas = 148;        // CTAs that share one call's tiles (and partials in the workspace)
 constexpr float kKvOff = 9.f, kKvRoom = 14.5f, kKvSlack = 1.5f;
@@ -465,7 +469,8 @@ __global__ void __launch_bounds__(KvAttnCfg<D>::kWarps * 32, 1) kv_attn_kernel(c
                    : nullptr;
         if (!fine && lane == 0) kv_error(a.at.err, kErrKvPlace);
     };
-    // a step reads the cache once: it should not push out of L2 what is read again, this kernel's code first of all
+    // a step reads the cache once (with several blocks of columns once a block): it should not push out of L2 what is
+    // read again, this kernel's code first of all
     uint64_t once;
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     auto copy = [&](int s, int u, int tiles) {      // `tiles` tiles from src on, to place u of stage s

@@ -138,8 +138,8 @@ size_t part_bytes(int head_dim)
 
 // Segments of at most this many tokens (as far as the page table reaches), one wave of them: a CTA takes one
 // each, and nothing goes through the workspace.  One sequence, 32 kv heads of 96, whole and split: 100 tokens
-// 5.8 and 11.4 us, 517 8.0 and 11.0, 1000 8.8 and 11.4, 2000 12.6 and 12.8; 8 kv heads of 128 with 4 query heads
-// each: 1000 tokens 9.8 and 12.3, 2000 tokens 14.2 and 12.8.
+// 5.8 and 11.4 us, 517 8.2 and 11.2, 1000 9.2 and 11.6, 2000 13.3 and 12.9; 8 kv heads of 128 with 4 query heads
+// each: 1000 tokens 10.5 and 12.6, 2000 tokens 15.3 and 13.2.
 constexpr int kWholeTokens = 1024;
 
 template <int D>
@@ -176,8 +176,8 @@ bool tma_map_heads(CUtensorMap *map, const uint16_t *base, int D, int heads, int
 
 // Where the items of one query tile fill at most half of the SMs, the keys of an item are split between the CTAs of a
 // cluster (2, 4 or 8), at least this many (of the average sequence) to each.  Whole and split: 137 queries, 2724 keys, 32
-// heads of 96, 40.4 and 26.7 us; 20 queries, 32020 keys, 32 heads of 128, 406 and 104; 64 queries, 32 heads, 1064 keys 20.3
-// and 14.5, 564 keys 13.5 and 12.1; 64 queries, 8 heads, 464 keys 11.7 and 11.9.  With 256 and 512 keys at least: 964 keys
+// heads of 96, 40.4 and 26.9 us; 20 queries, 32020 keys, 32 heads of 128, 406 and 105; 64 queries, 32 heads, 1064 keys 20.3
+// and 14.7, 564 keys 13.5 and 12.3; 64 queries, 8 heads, 464 keys 11.7 and 11.9.  With 256 and 512 keys at least: 964 keys
 // of 8 heads 14.9 and 18.0, with 128 11.3.
 constexpr int kSplitKeys = 128;
 
