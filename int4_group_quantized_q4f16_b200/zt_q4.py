@@ -580,7 +580,8 @@ class _Fill:
             self.captured = torch.cuda.is_current_stream_capturing()
             self.event = torch.cuda.Event()
             self.event.record(stream)
-        self.ordered = {stream.cuda_stream}       # handles of the streams that come behind the fill
+        # handles of the streams that come behind the fill; a captured one runs with its graph only
+        self.ordered = set() if self.captured else {stream.cuda_stream}
 
     def order(self, stream, capturing) -> bool:
         """Makes `stream` wait for the fill; whether that holds for its later work too."""

@@ -683,8 +683,9 @@ def test_plans_made_in_a_capture(zt):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for o in outs) and cache.errors() == 0
-    with pytest.raises(RuntimeError, match="captured"):
-        plans[0].run()
+    for stream in (None, main, fork):
+        with pytest.raises(RuntimeError, match="captured"):
+            plans[0].run(stream=stream)
 
 
 def test_attention_refuses_other_workspaces(zt):
